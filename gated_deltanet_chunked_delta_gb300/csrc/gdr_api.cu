@@ -29,6 +29,9 @@ int tc_fwd(const Params &p, int o_f32, int use_cp, cudaStream_t st);
 int tc_bwd(const Params &p, int use_cp, cudaStream_t st);
 int tc_supported(int K, int V);
 unsigned tc_take_status(cudaStream_t st);
+unsigned conv_take_status(cudaStream_t st);
+unsigned ssm_take_status(cudaStream_t st);
+unsigned fp8_take_status(cudaStream_t st);
 }  // namespace gdr
 
 namespace {
@@ -470,7 +473,8 @@ int gdr_check_status(void *stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(st) != cudaSuccess)
         return fail(GDR_ERR_CUDA, "stream error: %s", cudaGetErrorString(cudaGetLastError()));
-    const unsigned s = simt_take_status(st) | tc_take_status(st);
+    const unsigned s = simt_take_status(st) | tc_take_status(st) | conv_take_status(st) | ssm_take_status(st) |
+                       fp8_take_status(st);
     if (s & 0x80000000u) return fail(GDR_ERR_CUDA, "could not read the device status word");
     if (s & 1u) return fail(GDR_ERR_TIMEOUT, "a device-side wait ran out of polls");
     if (s & 2u) return fail(GDR_ERR_DEVICE, "a device-side index check failed");

@@ -210,6 +210,162 @@ GDR_API int gdr_fwd_noalloc(const gdr_shape *shape, gdr_buf q, gdr_buf k, gdr_bu
                             const float *beta, float scale, const float *h0, gdr_buf o, float *final_state,
                             float *A, float *h, const gdr_opts *opts, void *stream);
 
+/*
+ * Layer operators around a recurrent mixer
+ * ----------------------------------------
+ * What a layer runs before and after its token mixer, and the mixer with a
+ * diagonal transition: the short causal convolution, the selective state
+ * space scan, the root-mean-square norm of a residual stream (in 8 bits with
+ * scales, or in the input's type) and the product of 8-bit activations with
+ * 8-bit weights.  Ownership, execution and errors are as above.  Element
+ * types: `dtype` is GDR_BF16 or GDR_F32 for the activations of a call;
+ * parameters, recurrent states and their gradients are fp32 throughout.
+ * Activations are [B, T, ...] with a contiguous innermost part and free
+ * strides (in elements) between tokens (`*_row`) and batch rows (`*_batch`),
+ * so that slices of one projection's output are read in place; what a call
+ * writes is contiguous.  Packed sequences: `cu_seqlens` (device, int32,
+ * [n_seqs + 1], rising from 0 to T) with B = 1, else null and n_seqs = B
+ * sequences of T tokens.  No host copy of the bounds is needed: a call whose
+ * bounds do not rise from 0 to T reads and writes nothing outside its
+ * tensors, its results are unspecified, and gdr_check_status reports
+ * GDR_ERR_DEVICE.
+ */
+
+/* Short causal convolution along the tokens, depthwise:
+ *     pre_t = bias + sum_j weight[:, j] x_{t - W + 1 + j},   y_t = silu(pre_t) (or pre_t),
+ * where the inputs before a sequence are its initial state (zeros when null).
+ * State: the last W - 1 inputs of a sequence, oldest first, in `dtype`. */
+typedef struct {
+    const void *x;              /* [B, T, D], x_row, x_batch */
+    const float *weight, *bias; /* [D, W], [D] (nullable) */
+    const void *h0;             /* [n_seqs, W - 1, D], nullable */
+    const int32_t *cu_seqlens;
+    long long B, T, D, n_seqs, x_row, x_batch;
+    int W, dtype, silu;         /* W in {2, 3, 4}; silu: 1 with, 0 without the activation */
+    void *y;                    /* [B, T, D] (forward) */
+    void *ht;                   /* [n_seqs, W - 1, D], nullable (forward) */
+    /* backward: gradients of y (contiguous), of ht (nullable); of x, weight, bias, h0 (the last two nullable) */
+    const void *dy, *dht;
+    void *dx;
+    float *dweight, *dbias;
+    void *dh0;
+    void *workspace;            /* gdr_conv_bwd_workspace_size bytes, 16-byte aligned */
+    size_t workspace_bytes;
+} gdr_conv_args;
+GDR_API int gdr_conv_fwd(const gdr_conv_args *args, void *stream);
+GDR_API size_t gdr_conv_bwd_workspace_size(long long B, long long T, long long D, int W);
+GDR_API int gdr_conv_bwd(const gdr_conv_args *args, void *stream);
+
+/* One token for each of `rows` sequences.  Row r uses and updates state slot
+ * slots[r] (null: slot r).  A negative slot marks an idle row: its y is zero
+ * and no state changes.  A slot past n_slots is treated the same and reported
+ * by gdr_check_status (GDR_ERR_DEVICE).  A slot may appear once. */
+typedef struct {
+    const void *x;              /* [rows, D], x_row */
+    const float *weight, *bias;
+    void *state;                /* [n_slots, W - 1, D] */
+    const int32_t *slots;       /* [rows], nullable */
+    long long rows, D, n_slots, x_row;
+    int W, dtype, silu;
+    void *y;                    /* [rows, D] */
+} gdr_conv_step_args;
+GDR_API int gdr_conv_step(const gdr_conv_step_args *args, void *stream);
+
+/* Selective state space scan.  For every sequence and channel d of group
+ * g = d / (D / G), with s_t = softplus(dt_t + dt_bias) (or dt_t + dt_bias):
+ *     h_t = e^{s_t A} h_{t-1} + s_t x_t B_t,   u_t = C_t . h_t + skip x_t,   y_t = u_t silu(z_t) (or u_t).
+ * `states` (nullable) keeps h before every GDR_SSM_STRIDE-th token of every
+ * batch row for the backward. */
+#define GDR_SSM_STRIDE 16
+typedef struct {
+    const void *x, *dt, *z;     /* [B, T, D]; z nullable */
+    const void *Bm, *Cm;        /* [B, T, G, N], G and N contiguous */
+    const float *A, *skip, *dt_bias; /* [D, N], [D] (nullable), [D] (nullable) */
+    const float *h0;            /* [n_seqs, D, N], nullable */
+    const int32_t *cu_seqlens;
+    long long B, T, D, G, n_seqs;
+    long long x_row, x_batch, dt_row, dt_batch, z_row, z_batch, b_row, b_batch, c_row, c_batch;
+    int N, dtype, softplus;     /* N in {8, 16, 32, 64}; softplus: 1 with, 0 without */
+    void *y;                    /* [B, T, D] (forward) */
+    float *ht;                  /* [n_seqs, D, N], nullable (forward) */
+    float *states;              /* [B, ceil(T / 16), D, N]: written by the forward, read by the backward */
+    /* backward */
+    const void *dy;             /* [B, T, D] contiguous */
+    const float *dht;           /* nullable */
+    void *dx, *ddt, *dz;        /* [B, T, D]; dz iff z */
+    void *dB, *dC;              /* [B, T, G, N] */
+    float *dA, *dskip, *ddt_bias; /* dskip iff skip, ddt_bias iff dt_bias */
+    float *dh0;                 /* nullable */
+    void *workspace;            /* gdr_ssm_*_workspace_size bytes, 16-byte aligned (may be null when 0) */
+    size_t workspace_bytes;
+} gdr_ssm_args;
+GDR_API size_t gdr_ssm_fwd_workspace_size(const gdr_ssm_args *args);
+GDR_API int gdr_ssm_fwd(const gdr_ssm_args *args, void *stream);
+GDR_API size_t gdr_ssm_bwd_workspace_size(const gdr_ssm_args *args);
+GDR_API int gdr_ssm_bwd(const gdr_ssm_args *args, void *stream);
+
+/* One token for each of `rows` sequences; slots as in gdr_conv_step. */
+typedef struct {
+    const void *x, *dt, *z;     /* [rows, D]; z nullable */
+    const void *Bm, *Cm;        /* [rows, G, N] */
+    const float *A, *skip, *dt_bias;
+    float *state;               /* [n_slots, D, N] */
+    const int32_t *slots;
+    long long rows, D, G, n_slots, x_row, dt_row, z_row, b_row, c_row;
+    int N, dtype, softplus;
+    void *y;                    /* [rows, D] */
+} gdr_ssm_step_args;
+GDR_API int gdr_ssm_step(const gdr_ssm_step_args *args, void *stream);
+
+/* Root-mean-square norm of a residual stream:
+ *     r = x + residual (rounded to `dtype`; r = x when residual is null),
+ *     y = r rsqrt(mean(r^2) + eps) weight.
+ * Output y in `dtype`, or (q not null) in 8 bits (e4m3): for each row and
+ * block of 128 channels scale = max(max|y|, 1e-30) / 448 and q = y / scale,
+ * y not rounded in between.  Scales lie block by block, [ceil(D / 128), M], the
+ * order in which gdr_fp8_matmul reads them. */
+typedef struct {
+    const void *x, *residual;   /* [M, D], x_row, r_row; residual nullable */
+    const float *weight;        /* [D] */
+    long long M, D, x_row, r_row;
+    float eps;
+    int dtype;
+    void *sum;                  /* [M, D] r; iff residual */
+    void *y;                    /* [M, D], or null with q */
+    void *q;                    /* [M, D] e4m3, or null with y */
+    float *scales;              /* iff q */
+} gdr_norm_args;
+GDR_API int gdr_norm_fwd(const gdr_norm_args *args, void *stream);
+
+/* Its gradient: dr (the gradient of x and of residual alike) from dy and dsum
+ * (nullable), and dweight.  All [M, D] contiguous; `r` is the forward's sum
+ * (or x). */
+typedef struct {
+    const void *r, *dy, *dsum;
+    const float *weight;
+    long long M, D;
+    float eps;
+    int dtype;
+    void *dr;
+    float *dweight;
+    void *workspace;            /* gdr_norm_bwd_workspace_size bytes, 16-byte aligned */
+    size_t workspace_bytes;
+} gdr_norm_bwd_args;
+GDR_API size_t gdr_norm_bwd_workspace_size(long long M, long long D);
+GDR_API int gdr_norm_bwd(const gdr_norm_bwd_args *args, void *stream);
+
+/* out[m, n] = sum_kb a_scales[kb, m] b_scales[n / 128, kb] sum_{k in block kb} a[m, k] b[n, k]:
+ * e4m3 operands, blocks of 128 along k (the last may be short), sums in fp32.
+ * K a multiple of 16; a, b 16-byte aligned. */
+typedef struct {
+    const void *a, *b;          /* [M, K], [N, K] e4m3 */
+    const float *a_scales, *b_scales; /* [ceil(K / 128), M], [ceil(N / 128), ceil(K / 128)] */
+    long long M, N, K;
+    int out_dtype;              /* GDR_BF16 or GDR_F32 */
+    void *out;                  /* [M, N] */
+} gdr_fp8_args;
+GDR_API int gdr_fp8_matmul(const gdr_fp8_args *args, void *stream);
+
 /* Synchronises `stream`, then reads and clears the device status word:
  * GDR_OK, GDR_ERR_TIMEOUT, GDR_ERR_DEVICE, or GDR_ERR_CUDA. */
 GDR_API int gdr_check_status(void *stream);
