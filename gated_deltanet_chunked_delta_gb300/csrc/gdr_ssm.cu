@@ -8,13 +8,15 @@
 //     dx = s (e . B) + skip du,  ds = x (e . B) + f . A,  dA = sum f s,
 //     dB = sum_d e s x,  dC = sum_d h du,  dz = dy u silu'(z).
 //
-// Bound by arithmetic: T D N exponentials a pass (the special-function units)
-// and about five fp32 operations beside each, against 8 bytes of bf16 a (t, d).
-// So a state stays in registers (four neighbouring states of a channel a
-// thread, pairs in packed fp32 instructions), the per-(t, d) functions
-// (softplus, silu) are evaluated once, by the thread that loads the element,
-// and the sums over a channel's lanes are transposed (each lane ends with one
-// token's sum) instead of repeated in every lane.
+// Bound by arithmetic: T D N exponentials a pass (the special-function units
+// take 4 cycles for a warp's, packed fp32 pairs 2, both measured) and about
+// five fp32 operations beside each, against 8 bytes of bf16 a (t, d).  So a
+// state stays in registers (four neighbouring states of a channel a lane, pairs
+// in packed fp32 instructions), and a CTA's warps are split by role: four scan,
+// one an SM quarter, and do nothing else; four more read the next tile of
+// tokens (softplus and silu are evaluated there, once a (t, d)) and finish the
+// tile before (sums over a channel's lanes, skip, gate).  The roles meet at one
+// barrier a tile, over double buffers.
 //
 // Where sequences x channels leave SMs idle the tokens are cut into segments:
 // a summary pass gives each segment's end state from a zero start, and as the
@@ -28,9 +30,10 @@ namespace {
 
 __device__ unsigned g_ssm_status;
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;          // scanning threads; as many help
 constexpr int kTile = 32;              // tokens staged at a time (forward)
 constexpr int kBack = GDR_SSM_STRIDE;  // tokens of a backward tile, and between checkpoints
+constexpr int kGroup = 4;              // tokens of a backward tile whose latencies overlap
 
 struct SsmP {
     const void *x, *dt, *z, *Bm, *Cm, *dy;
@@ -44,36 +47,7 @@ struct SsmP {
     int B, T, D, G, Dg, tiles, S, seg_len, softplus;  // tiles: channel tiles of a group
 };
 
-// Sum over the lanes of a channel of kL values each: lane q ends with the sum of value q.
-template <int kL>
-__device__ __forceinline__ float lane_sums(float (&v)[kL], int q) {
-#pragma unroll
-    for (int step = kL / 2; step >= 1; step /= 2) {
-        const bool up = q & step;
-#pragma unroll
-        for (int i = 0; i < step; ++i) {
-            const float keep = up ? v[i + step] : v[i], send = up ? v[i] : v[i + step];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, step);
-        }
-    }
-    return v[0];
-}
-// Sum over the kC channels of a warp (lanes kL apart) of four states at kC
-// tokens: the lanes of channel c end with token c's sums in v[0].
-template <int kL, int kC>
-__device__ __forceinline__ void channel_sums(float (&v)[kC][4], int c) {
-#pragma unroll
-    for (int step = kC / 2; step >= 1; step /= 2) {
-        const bool up = c & step;
-#pragma unroll
-        for (int i = 0; i < step; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float keep = up ? v[i + step][k] : v[i][k], send = up ? v[i][k] : v[i + step][k];
-                v[i][k] = keep + __shfl_xor_sync(0xffffffffu, send, step * kL);
-            }
-    }
-}
+__device__ __forceinline__ f32x2 dup(float v) { return mk2(v, v); }
 
 struct State {  // four neighbouring states
     f32x2 a, b;
@@ -95,22 +69,23 @@ __device__ __forceinline__ float dot(const State &x, const State &y) {
     return lo + hi;
 }
 // e^{s A} of four states, A2 = A log2 e
-__device__ __forceinline__ State decay(const State &A2, float s) {
-    const f32x2 s2 = mk2(s, s);
+__device__ __forceinline__ State decay(const State &A2, f32x2 s2) {
     float a, b, c, d;
     un2(mul2(A2.a, s2), a, b);
     un2(mul2(A2.b, s2), c, d);
     return State{mk2(ex2f(a), ex2f(b)), mk2(ex2f(c), ex2f(d))};
 }
-__device__ __forceinline__ State advance(const State &a, const State &h, float in, const State &Bt) {
-    const f32x2 i2 = mk2(in, in);
+__device__ __forceinline__ State advance(const State &a, const State &h, f32x2 i2, const State &Bt) {
     return State{fma2(a.a, h.a, mul2(i2, Bt.a)), fma2(a.b, h.b, mul2(i2, Bt.b))};
 }
 
 // Where a thread works: channel d (states n0 .. n0 + 3), whether it exists.
+// Neighbouring lanes are neighbouring channels and share their states' place:
+// 16-byte reads of B and C then cost 2 cycles of the shared-memory pipe; 4 with
+// the states' places across neighbouring lanes (both measured).
 template <int kL>
 struct Place {
-    static constexpr int kCh = kThreads / kL, kN = 4 * kL;
+    static constexpr int kCh = kThreads / kL, kN = 4 * kL, kC = 32 / kL;  // kC: channels of a warp
     int g, gt, c0, nch, ch, q, d, n0;
     bool on;
     __device__ __forceinline__ explicit Place(const SsmP &p) {
@@ -118,8 +93,8 @@ struct Place {
         g = gt / p.tiles;
         c0 = g * p.Dg + (gt % p.tiles) * kCh;
         nch = min(kCh, (g + 1) * p.Dg - c0);
-        ch = threadIdx.x / kL;
-        q = threadIdx.x % kL;
+        ch = threadIdx.x % kThreads / 32 * kC + threadIdx.x % kC;
+        q = threadIdx.x % 32 / kC;
         on = ch < nch;
         d = c0 + (on ? ch : 0);
         n0 = 4 * q;
@@ -145,7 +120,8 @@ __device__ __forceinline__ State chain(const SsmP &p, const Place<kL> &w, const 
     if (!w.on) return v;
     for (int j = j0; j != seg; j += step) {
         const long long row = (long long)b * p.S + j;
-        const State a = decay(A2, p.sum_s[row * p.D + w.d]);
+        const float sum = p.sum_s[row * p.D + w.d];
+        const State a = decay(A2, dup(sum));
         const State e = load_state(p.sum_h + w.at(row, p));
         v = State{fma2(a.a, v.a, e.a), fma2(a.b, v.b, e.b)};
     }
@@ -160,36 +136,202 @@ __device__ __forceinline__ State load_A2(const SsmP &p, const Place<kL> &w, Stat
     return State{mul2(a.a, k), mul2(a.b, k)};
 }
 
+// Eight neighbouring channels of one token as packed pairs.
+template <typename T>
+__device__ __forceinline__ void get8(const Raw8<T> &r, f32x2 (&v)[4]) {
+    float f[8];
+    unpack8(r, f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = mk2(f[2 * k], f[2 * k + 1]);
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void put8(T *p, const f32x2 (&v)[4], int n) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) un2(v[k], f[2 * k], f[2 * k + 1]);
+    store8<T, kVec>(p, f, n);
+}
+// Parameters of eight channels, zeros where there are none.
+__device__ __forceinline__ void param8(const float *p, int n, f32x2 (&v)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = mk2(p && 2 * k < n ? p[2 * k] : 0.f, p && 2 * k + 1 < n ? p[2 * k + 1] : 0.f);
+}
+// A helper owns eight channels of a token, 128 bytes of 16-byte entries, and
+// its neighbours the next ones: entry e of them lies at place e ^ place_key, so
+// that eight threads' accesses to their e-th entries fall into eight different
+// bank groups.
+template <int kCh>
+__device__ __forceinline__ int place_key(int row, int ch) { return (row * (kCh / 8) + ch / 8) & 7; }
+template <int kCh>
+__device__ __forceinline__ int place(int row, int ch) { return ch ^ place_key<kCh>(row, ch); }
+// The same for 8-byte entries, moved two at a time.
+template <int kCh>
+__device__ __forceinline__ int pair_key(int row, int ch) { return (row * (kCh / 8) + ch / 8) & 6; }
+template <int kCh>
+__device__ __forceinline__ int pair_place(int row, int ch) { return ch ^ pair_key<kCh>(row, ch); }
+// The scalar functions of gdr_layer.h for two values at once.
+__device__ __forceinline__ f32x2 softplus2(f32x2 v) {
+    float a, b;
+    un2(v, a, b);
+    const float ua = ex2f(-kLog2e * fabsf(a)), ub = ex2f(-kLog2e * fabsf(b));
+    float da, db;
+    un2(add2(mk2(ua, ub), dup(2.f)), da, db);
+    const f32x2 s = mul2(mk2(ua, ub), mk2(rcpf(da), rcpf(db))), s2 = mul2(s, s);
+    f32x2 p = fma2(s2, dup(1.f / 13), dup(1.f / 11));
+    p = fma2(s2, p, dup(1.f / 9));
+    p = fma2(s2, p, dup(1.f / 7));
+    p = fma2(s2, p, dup(1.f / 5));
+    p = fma2(s2, p, dup(1.f / 3));
+    p = fma2(s2, p, dup(1.f));
+    return fma2(add2(s, s), p, mk2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
+    float a, b;
+    un2(mul2(v, dup(-kLog2e)), a, b);
+    un2(add2(mk2(ex2f(a), ex2f(b)), dup(1.f)), a, b);
+    return mk2(rcpf(a), rcpf(b));
+}
+// Sum of a channel's kL partial sums, which lie together.
+template <int kL>
+__device__ __forceinline__ float lane_sum(const float *p) {
+    if (kL == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        return v.x + v.y;
+    }
+    float4 v = *reinterpret_cast<const float4 *>(p);
+#pragma unroll
+    for (int i = 4; i < kL; i += 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(p + i);
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    }
+    return (v.x + v.y) + (v.z + v.w);
+}
+
 // Forward, or (kSum) the segments' summaries.
+template <int kL, bool kSum>
+struct FwdSmem {
+    static constexpr int kCh = kThreads / kL, kN = 4 * kL;
+    float2 in[2][kTile][kCh];  // s, s x
+    float B[2][kTile][kN];
+    float C[kSum ? 1 : 2][kTile][kN];
+    float part[kSum ? 1 : 2][kTile][kCh][kL];  // C . h, a lane's part
+};
+
 template <typename T, int kL, bool kVec, bool kSum>
-__global__ void __launch_bounds__(kThreads) k_ssm_fwd(const SsmP p) {
+__global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_fwd(const SsmP p) {
     using W = Place<kL>;
     constexpr int kCh = W::kCh, kN = W::kN;
-    constexpr int kVecs = kTile * kCh / 8, kNV = (kVecs + kThreads - 1) / kThreads;
-    constexpr int kBV = kTile * kN / 8, kNB = ((kSum ? 1 : 2) * kBV + kThreads - 1) / kThreads;
-    constexpr int kPad = 32 / kL < 4 ? 4 : 32 / kL;
-    __shared__ __align__(16) float2 s_in[kTile][kCh];  // s, s x
-    __shared__ __align__(16) float s_B[kTile][kN], s_C[kSum ? 1 : kTile][kN];
-    __shared__ __align__(16) float s_y[kSum ? 1 : kTile][kCh + kPad];
-    __shared__ __align__(16) float s_bias[kCh], s_skip[kCh];
+    extern __shared__ __align__(16) char smem_raw[];
+    FwdSmem<kL, kSum> &sm = *reinterpret_cast<FwdSmem<kL, kSum> *>(smem_raw);
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_bounds(p.seqs, &g_ssm_status);
     const W w(p);
-    const int tid = threadIdx.x, seg = blockIdx.y, b = blockIdx.z;
-    const int ts = seg * p.seg_len, te = min(ts + p.seg_len, p.T);
-    const int sbase = p.seqs.cu ? 0 : b;
-    const T *x = static_cast<const T *>(p.x) + b * p.x_batch + w.c0;
-    const T *dt = static_cast<const T *>(p.dt) + b * p.dt_batch + w.c0;
-    const T *z = p.z ? static_cast<const T *>(p.z) + b * p.z_batch + w.c0 : nullptr;
-    const T *Bm = static_cast<const T *>(p.Bm) + b * p.b_batch + (long long)w.g * kN;
-    const T *Cm = static_cast<const T *>(p.Cm) + b * p.c_batch + (long long)w.g * kN;
-    T *y = static_cast<T *>(p.y) + (long long)b * p.T * p.D + w.c0;
-    for (int i = tid; i < kCh; i += kThreads) {
-        s_bias[i] = p.dt_bias && i < w.nch ? p.dt_bias[w.c0 + i] : 0.f;
-        s_skip[i] = p.skip && i < w.nch ? p.skip[w.c0 + i] : 0.f;
-    }
-    __syncthreads();  // the first tile is staged with them
-    const State A2 = load_A2<kL>(p, w, nullptr);
+    const int seg = blockIdx.y, b = blockIdx.z;
+    const int ts = seg * p.seg_len, te = min(ts + p.seg_len, p.T), tiles = (te - ts + kTile - 1) / kTile;
 
+    if (threadIdx.x >= kThreads) {  // ---- the helpers
+        constexpr int kItems = kTile * kCh / 8, kNI = (kItems + kThreads - 1) / kThreads;  // 8 channels of a token each
+        constexpr int kBV = kTile * kN / 8, kNB = ((kSum ? 1 : 2) * kBV + kThreads - 1) / kThreads;
+        constexpr int kRows = kThreads / (kCh / 8);  // tokens from a thread's item to its next
+        const int ht = threadIdx.x - kThreads;
+        const int c = ht % (kCh / 8) * 8, row0 = ht / (kCh / 8), nv = min(8, w.nch - c);
+        const T *x = static_cast<const T *>(p.x) + b * p.x_batch + w.c0 + c;
+        const T *dt = static_cast<const T *>(p.dt) + b * p.dt_batch + w.c0 + c;
+        const T *z = p.z ? static_cast<const T *>(p.z) + b * p.z_batch + w.c0 + c : nullptr;
+        const T *Bm = static_cast<const T *>(p.Bm) + b * p.b_batch + (long long)w.g * kN;
+        const T *Cm = static_cast<const T *>(p.Cm) + b * p.c_batch + (long long)w.g * kN;
+        T *y = static_cast<T *>(p.y) + (long long)b * p.T * p.D + w.c0 + c;
+        f32x2 bias[4], skip[4];
+        param8(p.dt_bias ? p.dt_bias + w.c0 + c : nullptr, nv, bias);
+        param8(p.skip ? p.skip + w.c0 + c : nullptr, nv, skip);
+        struct Fetched {
+            Raw8<T> x[kNI], dt[kNI], z[kNI], bc[kNB];
+        };
+        auto fetch = [&](int tb, Fetched &f) {
+#pragma unroll
+            for (int i = 0; i < kNI; ++i) {
+                const int row = tb + row0 + i * kRows, n = ht + i * kThreads < kItems && row < te ? nv : 0;
+                f.x[i] = load8<T, kVec>(x + row * p.x_row, n);
+                f.dt[i] = load8<T, kVec>(dt + row * p.dt_row, n);
+                if (!kSum && z) f.z[i] = load8<T, kVec>(z + row * p.z_row, n);
+            }
+#pragma unroll
+            for (int i = 0; i < kNB; ++i) {
+                const int v = ht + i * kThreads, r = v % kBV, row = tb + r / (kN / 8), col = (r % (kN / 8)) * 8;
+                const int n = v < (kSum ? 1 : 2) * kBV && row < te ? 8 : 0;
+                if (v >= kBV) f.bc[i] = load8<T, kVec>(Cm + row * p.c_row + col, n);
+                else f.bc[i] = load8<T, kVec>(Bm + row * p.b_row + col, n);
+            }
+        };
+        auto stage = [&](int tb, int buf, const Fetched &f) {
+#pragma unroll
+            for (int i = 0; i < kNI; ++i) {
+                if (ht + i * kThreads >= kItems) continue;
+                const int row = row0 + i * kRows, key = pair_key<kCh>(row, c);
+                const bool real = tb + row < te;  // past the end: no decay, no input
+                f32x2 xv[4], dv[4];
+                get8(f.x[i], xv);
+                get8(f.dt[i], dv);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f32x2 st = add2(dv[k], bias[k]);
+                    if (p.softplus) st = softplus2(st);
+                    if (!real) st = dup(0.f);
+                    float s0, s1, i0, i1;
+                    un2(st, s0, s1);
+                    un2(mul2(st, xv[k]), i0, i1);
+                    *reinterpret_cast<float4 *>(&sm.in[buf][row][c + ((2 * k) ^ key)]) = make_float4(s0, i0, s1, i1);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kNB; ++i) {
+                const int v = ht + i * kThreads, r = v % kBV, row = r / (kN / 8), col = (r % (kN / 8)) * 8;
+                if (v >= (kSum ? 1 : 2) * kBV) continue;
+                float g[8];
+                unpack8(f.bc[i], g);
+                float *to = !kSum && v >= kBV ? &sm.C[kSum ? 0 : buf][row][col] : &sm.B[buf][row][col];
+                *reinterpret_cast<float4 *>(to) = make_float4(g[0], g[1], g[2], g[3]);
+                *reinterpret_cast<float4 *>(to + 4) = make_float4(g[4], g[5], g[6], g[7]);
+            }
+        };
+        // Tiles in flight: the one to finish, the one being scanned, the one to
+        // stage, and the one being fetched.
+        Fetched done, now, next, then;
+        fetch(ts, now);
+        if (tiles > 1) fetch(ts + kTile, next);
+        stage(ts, 0, now);
+        __syncthreads();
+        for (int i = 0; i <= tiles; ++i) {
+            if (i + 2 < tiles) fetch(ts + (i + 2) * kTile, then);
+            if (i + 1 < tiles) stage(ts + (i + 1) * kTile, (i + 1) & 1, next);
+            if (!kSum && i > 0) {
+                const int tp = ts + (i - 1) * kTile;
+#pragma unroll
+                for (int j = 0; j < kNI; ++j) {
+                    const int row = row0 + j * kRows, key = place_key<kCh>(row, c);
+                    if (ht + j * kThreads >= kItems || tp + row >= te || nv <= 0) continue;
+                    f32x2 xv[4], zv[4], u[4];
+                    get8(done.x[j], xv);
+                    if (z) get8(done.z[j], zv);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float(*part)[kL] = &sm.part[kSum ? 0 : (i - 1) & 1][row][c];
+                        u[k] = fma2(skip[k], xv[k], mk2(lane_sum<kL>(part[(2 * k) ^ key]), lane_sum<kL>(part[(2 * k + 1) ^ key])));
+                        if (z) u[k] = mul2(u[k], mul2(zv[k], sigmoid2(zv[k])));
+                    }
+                    put8<T, kVec>(y + (long long)(tp + row) * p.D, u, nv);
+                }
+            }
+            done = now;
+            now = next;
+            next = then;
+            if (i < tiles) __syncthreads();
+        }
+        return;
+    }
+
+    // ---- the scan
+    const int sbase = p.seqs.cu ? 0 : b;
+    const State A2 = load_A2<kL>(p, w, nullptr);
     int n = p.seqs.find(ts), s0 = p.seqs.bound(n), s1 = p.seqs.bound(n + 1);
     State h;
     if (ts <= s0) h = start_state<kL>(p, w, sbase + n);
@@ -197,125 +339,60 @@ __global__ void __launch_bounds__(kThreads) k_ssm_fwd(const SsmP p) {
     if (!kSum && seg == 0 && p.seqs.cu)
         for (int m = 0; m < p.seqs.n && p.seqs.bound(m + 1) <= 0; ++m) pass_state<kL>(p, w, p.h0, p.ht, m);
     float total = 0.f;
-
-    Raw8<T> rx[kNV], rd[kNV], rz[kNV], rb[kNB], cx[kNV], cz[kNV];
-    auto fetch = [&](int tb) {
-#pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            const int v = tid + i * kThreads, row = tb + v / (kCh / 8), col = (v % (kCh / 8)) * 8;
-            const int nv = v < kVecs && row < te ? min(8, w.nch - col) : 0;
-            rx[i] = load8<T, kVec>(x + row * p.x_row + col, nv);
-            rd[i] = load8<T, kVec>(dt + row * p.dt_row + col, nv);
-            if (!kSum && z) rz[i] = load8<T, kVec>(z + row * p.z_row + col, nv);
-        }
-#pragma unroll
-        for (int i = 0; i < kNB; ++i) {
-            const int v = tid + i * kThreads, r = v % kBV, row = tb + r / (kN / 8), col = (r % (kN / 8)) * 8;
-            const bool is_c = v >= kBV;
-            rb[i] = load8<T, kVec>(is_c ? Cm + row * p.c_row + col : Bm + row * p.b_row + col,
-                                   v < (kSum ? 1 : 2) * kBV && row < te ? 8 : 0);
-        }
-    };
-    fetch(ts);
-    for (int tb = ts; tb < te; tb += kTile) {
-#pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            const int v = tid + i * kThreads, row = v / (kCh / 8), col = (v % (kCh / 8)) * 8;
-            cx[i] = rx[i];
-            if (!kSum && z) cz[i] = rz[i];
-            if (v >= kVecs) continue;
-            float fx[8], fd[8];
-            unpack8(rx[i], fx);
-            unpack8(rd[i], fd);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                float s[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float raw = fd[e + k] + s_bias[col + e + k];
-                    s[k] = p.softplus ? softplusf(raw) : raw;
-                }
-                *reinterpret_cast<float4 *>(&s_in[row][col + e]) = make_float4(s[0], s[0] * fx[e], s[1], s[1] * fx[e + 1]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kNB; ++i) {
-            const int v = tid + i * kThreads, r = v % kBV, row = r / (kN / 8), col = (r % (kN / 8)) * 8;
-            if (v >= (kSum ? 1 : 2) * kBV) continue;
-            float f[8];
-            unpack8(rb[i], f);
-            float *to = !kSum && v >= kBV ? &s_C[kSum ? 0 : row][col] : &s_B[row][col];
-            *reinterpret_cast<float4 *>(to) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4 *>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        }
-        __syncthreads();
-        if (tb + kTile < te) fetch(tb + kTile);
-
-        const int tend = min(tb + kTile, te);
+    const long long ck0 = (long long)b * ((p.T + kBack - 1) / kBack);
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        const int tb = ts + i * kTile, buf = i & 1;
         auto keep = [&](int t) {  // the checkpoint before token t
-            if (!kSum && p.states && (t & (kBack - 1)) == 0 && w.on)
-                store_state(p.states + w.at((long long)b * ((p.T + kBack - 1) / kBack) + t / kBack, p), h);
+            if (!kSum && p.states && w.on) store_state(p.states + w.at(ck0 + t / kBack, p), h);
         };
-        auto token = [&](int i) {
-            const float2 in = s_in[i][w.ch];
-            h = advance(decay(A2, in.x), h, in.y, load_state(&s_B[i][w.n0]));
-            total += in.x;
-            return kSum ? 0.f : dot(h, load_state(&s_C[kSum ? 0 : i][w.n0]));
+        auto one = [&](int r) {
+            const float2 in = sm.in[buf][r][pair_place<kCh>(r, w.ch)];
+            h = advance(decay(A2, dup(in.x)), h, dup(in.y), load_state(&sm.B[buf][r][w.n0]));
+            if (kSum) total += in.x;
+            return kSum ? 0.f : dot(h, load_state(&sm.C[kSum ? 0 : buf][r][w.n0]));
         };
-        auto single = [&](int t) {
-            keep(t);
-            float u = token(t - tb);
-            if (kSum) return;
-#pragma unroll
-            for (int m = kL / 2; m >= 1; m /= 2) u += __shfl_xor_sync(0xffffffffu, u, m);
-            if (w.q == 0) s_y[kSum ? 0 : t - tb][w.ch] = u;
+        auto put = [&](int r, float u) {
+            if (!kSum) sm.part[kSum ? 0 : buf][r][place<kCh>(r, w.ch)][w.q] = u;
         };
-        for (int t = tb; t < tend;) {
-            if (t >= s1 && n + 1 < p.seqs.count()) {
-                do {
-                    ++n;
-                    s0 = s1;
-                    s1 = p.seqs.bound(n + 1);
-                } while (s1 <= t && n + 1 < p.seqs.count());
-                h = start_state<kL>(p, w, sbase + n);
-            }
-            const int to = s1 > t ? min(tend, s1) : tend;
-            while (t < to && t % kL) single(t++);
-            for (; t + kL <= to; t += kL) {
-                keep(t);
-                float u[kL];
-#pragma unroll
-                for (int i = 0; i < kL; ++i) u[i] = token(t - tb + i);
-                if (!kSum) {
-                    const float mine = lane_sums<kL>(u, w.q);
-                    s_y[kSum ? 0 : t - tb + w.q][w.ch] = mine;
+        const int tend = min(tb + kTile, te);
+        if (p.seqs.cu && s1 < tend) {  // a sequence ends inside the tile, or ended before it
+            for (int t = tb; t < tend;) {
+                if (t >= s1 && n + 1 < p.seqs.count()) {
+                    do {
+                        ++n;
+                        s0 = s1;
+                        s1 = p.seqs.bound(n + 1);
+                    } while (s1 <= t && n + 1 < p.seqs.count());
+                    h = start_state<kL>(p, w, sbase + n);
+                }
+                const int to = s1 > t ? min(tend, s1) : tend;
+                for (; t < to; ++t) {
+                    if (t % kBack == 0) keep(t);
+                    put(t - tb, one(t - tb));
+                }
+                if (!kSum && t == s1) {
+                    if (p.ht && w.on) store_state(p.ht + w.at(sbase + n, p), h);
+                    for (int m = n + 1; m < p.seqs.n && p.seqs.bound(m + 1) <= s1; ++m) pass_state<kL>(p, w, p.h0, p.ht, m);
                 }
             }
-            while (t < to) single(t++);
-            if (!kSum && t == s1) {
-                if (p.ht && w.on) store_state(p.ht + w.at(sbase + n, p), h);
+        } else {  // tokens past the end change nothing
+#pragma unroll 1
+            for (int g = 0; g < kTile; g += kBack) {
+                if (tb + g < te) keep(tb + g);
+                float u[kBack];  // stored after the last load: a store would hold back the loads behind it
+#pragma unroll
+                for (int r = 0; r < kBack; ++r) u[r] = one(g + r);
+#pragma unroll
+                for (int r = 0; r < kBack; ++r) put(g + r, u[r]);
+            }
+            if (!kSum && p.ht && tend == s1 && w.on) {
+                store_state(p.ht + w.at(sbase + n, p), h);
                 if (p.seqs.cu)
-                    for (int m = n + 1; m < p.seqs.n && p.seqs.bound(m + 1) <= s1; ++m)
-                        pass_state<kL>(p, w, p.h0, p.ht, m);
+                    for (int m = n + 1; m < p.seqs.n && p.seqs.bound(m + 1) <= s1; ++m) pass_state<kL>(p, w, p.h0, p.ht, m);
             }
         }
         __syncthreads();
-        if (!kSum) {
-#pragma unroll
-            for (int i = 0; i < kNV; ++i) {
-                const int v = tid + i * kThreads, row = v / (kCh / 8), col = (v % (kCh / 8)) * 8;
-                if (v >= kVecs || tb + row >= te || col >= w.nch) continue;
-                float fx[8], fz[8], o[8];
-                unpack8(cx[i], fx);
-                if (z) unpack8(cz[i], fz);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    o[e] = fmaf(s_skip[col + e], fx[e], s_y[kSum ? 0 : row][col + e]);
-                    if (z) o[e] *= fz[e] * sigmoidf(fz[e]);
-                }
-                store8<T, kVec>(y + (long long)(tb + row) * p.D + col, o, min(8, w.nch - col));
-            }
-        }
     }
     if (kSum && w.on) {
         const long long row = (long long)b * p.S + seg;
@@ -325,42 +402,247 @@ __global__ void __launch_bounds__(kThreads) k_ssm_fwd(const SsmP p) {
 }
 
 // Backward, or (kSum) the segments' reverse summaries.  Tiles of kBack tokens
-// from the segment's end: the states of a tile are recomputed from its
-// checkpoint and kept in registers with their decays, then the gradient runs
-// back over them.
+// from the segment's end: a scanning lane recomputes the states of a tile from
+// its checkpoint, keeps them in registers, and runs the gradient back over
+// them (the decays are formed again: the special-function units have room, the
+// registers have not).
+//
+// dB and dC are sums over channels, which lie across lanes: two exchanges leave
+// every lane with one state's sum over four channels, the helpers add the rest.
+template <int kL, bool kSum>
+struct BwdSmem {
+    static constexpr int kCh = kThreads / kL, kN = 4 * kL, kC = 32 / kL;  // kC: channels of a warp
+    static constexpr int kFold = kC < 4 ? kC : 4, kParts = kThreads / 32 * (kC / kFold);
+    float2 in[2][kBack][kCh];  // s, s x
+    float du[2][kBack][kCh];
+    float B[2][kBack][kN], C[2][kBack][kN];
+    float u[kSum ? 1 : 2][kBack][kCh][kL], eb[kSum ? 1 : 2][kBack][kCh][kL], fa[kSum ? 1 : 2][kBack][kCh][kL];
+    float dB[kSum ? 1 : 2][kBack][kParts][kN], dC[kSum ? 1 : 2][kBack][kParts][kN];
+};
+
+// The sum over kFold neighbouring lanes of four states: lane m of them ends
+// with state m's (of two lanes, lane m with states 2 m and 2 m + 1).
+template <int kL>
+__device__ __forceinline__ float2 fold_channels(State v) {
+    constexpr int kC = 32 / kL, kFirst = kC >= 4 ? 2 : 1;
+    const bool up = threadIdx.x & kFirst;
+    float lo, hi;
+    un2(up ? v.a : v.b, lo, hi);
+    un2(add2(up ? v.b : v.a, mk2(__shfl_xor_sync(0xffffffffu, lo, kFirst), __shfl_xor_sync(0xffffffffu, hi, kFirst))), lo, hi);
+    if (kC >= 4) {
+        const bool odd = threadIdx.x & 1;
+        return make_float2((odd ? hi : lo) + __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1), 0.f);
+    }
+    return make_float2(lo, hi);
+}
+template <int kL>
+__device__ __forceinline__ void put_fold(float *to, float2 v) {
+    if (32 / kL >= 4) *to = v.x;
+    else *reinterpret_cast<float2 *>(to) = v;
+}
+
 template <typename T, int kL, bool kVec, bool kSum>
-__global__ void __launch_bounds__(kThreads) k_ssm_bwd(const SsmP p) {
+__global__ void __launch_bounds__(2 * kThreads, 1) k_ssm_bwd(const SsmP p) {
     using W = Place<kL>;
-    constexpr int kCh = W::kCh, kN = W::kN, kC = 32 / kL;  // kC: channels of a warp
-    constexpr int kVecs = kBack * kCh / 8;                 // of x and dt; as many of z and dy
-    constexpr int kNV = (2 * kVecs + kThreads - 1) / kThreads;
-    constexpr int kBV = kBack * kN / 8, kNB = (2 * kBV + kThreads - 1) / kThreads;
-    constexpr int kPad = 32 / kL < 4 ? 4 : 32 / kL;
-    constexpr int kWarps = kThreads / 32;
-    __shared__ __align__(16) float4 s_in[kBack][kCh];  // s, s x, du, x
-    __shared__ __align__(16) float s_B[kBack][kN], s_C[kBack][kN];
-    __shared__ __align__(16) float s_u[kSum ? 1 : kBack][kCh + kPad], s_eb[kSum ? 1 : kBack][kCh + kPad],
-        s_fa[kSum ? 1 : kBack][kCh + kPad];
-    __shared__ __align__(16) float s_dB[kSum ? 1 : kWarps][kBack][kN], s_dC[kSum ? 1 : kWarps][kBack][kN];
-    __shared__ __align__(16) float s_bias[kCh], s_skip[kCh];
+    using S = BwdSmem<kL, kSum>;
+    constexpr int kCh = W::kCh, kN = W::kN;
+    extern __shared__ __align__(16) char smem_raw[];
+    S &sm = *reinterpret_cast<S *>(smem_raw);
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_bounds(p.seqs, &g_ssm_status);
     const W w(p);
-    const int tid = threadIdx.x, b = blockIdx.z, warp = tid / 32, cw = (tid % 32) / kL;
-    const int seg = kSum ? blockIdx.y + 1 : blockIdx.y;  // nothing follows from the first segment's summary
-    const int ts = seg * p.seg_len, te = min(ts + p.seg_len, p.T);
-    const int sbase = p.seqs.cu ? 0 : b;
-    const T *x = static_cast<const T *>(p.x) + b * p.x_batch + w.c0;
-    const T *dt = static_cast<const T *>(p.dt) + b * p.dt_batch + w.c0;
-    const T *z = p.z ? static_cast<const T *>(p.z) + b * p.z_batch + w.c0 : nullptr;
-    const long long own = (long long)b * p.T * p.D + w.c0;
-    const T *dy = static_cast<const T *>(p.dy) + own;
-    const T *Bm = static_cast<const T *>(p.Bm) + b * p.b_batch + (long long)w.g * kN;
-    const T *Cm = static_cast<const T *>(p.Cm) + b * p.c_batch + (long long)w.g * kN;
-    for (int i = tid; i < kCh; i += kThreads) {
-        s_bias[i] = p.dt_bias && i < w.nch ? p.dt_bias[w.c0 + i] : 0.f;
-        s_skip[i] = p.skip && i < w.nch ? p.skip[w.c0 + i] : 0.f;
+    const int b = blockIdx.z, seg = kSum ? blockIdx.y + 1 : blockIdx.y;  // nothing follows from the first segment's summary
+    const int ts = seg * p.seg_len, te = min(ts + p.seg_len, p.T), tiles = (te - ts + kBack - 1) / kBack;
+    const long long srow = (long long)b * p.S + seg;
+
+    if (threadIdx.x >= kThreads) {  // ---- the helpers
+        // An item is eight channels of a token: of x and dt (items below kPer: s, dx, ddt) or of dy and z (du, dz).
+        constexpr int kPer = kBack * kCh / 8, kNI = (2 * kPer + kThreads - 1) / kThreads;
+        constexpr int kBV = kBack * kN / 8, kNB = (2 * kBV + kThreads - 1) / kThreads;
+        const int ht = threadIdx.x - kThreads;
+        const int c = ht % (kCh / 8) * 8, row = ht % kPer / (kCh / 8), nv = min(8, w.nch - c);
+        const int key = place_key<kCh>(row, c), key2 = pair_key<kCh>(row, c);
+        const T *x = static_cast<const T *>(p.x) + b * p.x_batch + w.c0 + c;
+        const T *dt = static_cast<const T *>(p.dt) + b * p.dt_batch + w.c0 + c;
+        const T *z = p.z ? static_cast<const T *>(p.z) + b * p.z_batch + w.c0 + c : nullptr;
+        const long long own = (long long)b * p.T * p.D + w.c0 + c;
+        const T *dy = static_cast<const T *>(p.dy) + own;
+        const T *Bm = static_cast<const T *>(p.Bm) + b * p.b_batch + (long long)w.g * kN;
+        const T *Cm = static_cast<const T *>(p.Cm) + b * p.c_batch + (long long)w.g * kN;
+        f32x2 bias[4], skip[4], gskip[4], gbias[4];
+        param8(p.dt_bias ? p.dt_bias + w.c0 + c : nullptr, nv, bias);
+        param8(p.skip ? p.skip + w.c0 + c : nullptr, nv, skip);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gskip[k] = gbias[k] = dup(0.f);
+        struct Fetched {
+            Raw8<T> x[kNI], g[kNI], bc[kNB];  // x; dt, or dy
+            Raw8<T> z[kNI];
+        };
+        auto fetch = [&](int tb, Fetched &f) {
+#pragma unroll
+            for (int i = 0; i < kNI; ++i) {
+                const int v = ht + i * kThreads, t = tb + row, n = v < 2 * kPer && t < te ? nv : 0;
+                f.x[i] = load8<T, kVec>(x + t * p.x_row, n);
+                if (v < kPer) f.g[i] = load8<T, kVec>(dt + t * p.dt_row, n);
+                else f.g[i] = load8<T, kVec>(dy + (long long)t * p.D, n);
+                if (z && v >= kPer) f.z[i] = load8<T, kVec>(z + t * p.z_row, n);
+            }
+#pragma unroll
+            for (int i = 0; i < kNB; ++i) {
+                const int v = ht + i * kThreads, r = v % kBV, t = tb + r / (kN / 8), col = (r % (kN / 8)) * 8;
+                const int n = v < 2 * kBV && t < te ? 8 : 0;
+                if (v >= kBV) f.bc[i] = load8<T, kVec>(Cm + t * p.c_row + col, n);
+                else f.bc[i] = load8<T, kVec>(Bm + t * p.b_row + col, n);
+            }
+        };
+        auto stage = [&](int tb, int buf, const Fetched &f) {
+#pragma unroll
+            for (int i = 0; i < kNI; ++i) {
+                const int v = ht + i * kThreads;
+                if (v >= 2 * kPer) continue;
+                f32x2 g[4];
+                get8(f.g[i], g);
+                if (v < kPer) {
+                    const bool real = tb + row < te;  // past the end: no decay, no input
+                    f32x2 xv[4];
+                    get8(f.x[i], xv);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        f32x2 st = add2(g[k], bias[k]);
+                        if (p.softplus) st = softplus2(st);
+                        if (!real) st = dup(0.f);
+                        float s0, s1, i0, i1;
+                        un2(st, s0, s1);
+                        un2(mul2(st, xv[k]), i0, i1);
+                        *reinterpret_cast<float4 *>(&sm.in[buf][row][c + ((2 * k) ^ key2)]) = make_float4(s0, i0, s1, i1);
+                    }
+                } else {
+                    if (z) {
+                        f32x2 zv[4];
+                        get8(f.z[i], zv);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) g[k] = mul2(g[k], mul2(zv[k], sigmoid2(zv[k])));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        float4 u;
+                        un2(g[k], u.x, u.y);
+                        un2(g[k + 1], u.z, u.w);
+                        *reinterpret_cast<float4 *>(&sm.du[buf][row][c + 2 * k]) = u;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kNB; ++i) {
+                const int v = ht + i * kThreads, r = v % kBV, rr = r / (kN / 8), col = (r % (kN / 8)) * 8;
+                if (v >= 2 * kBV) continue;
+                float g[8];
+                unpack8(f.bc[i], g);
+                float *to = v >= kBV ? &sm.C[buf][rr][col] : &sm.B[buf][rr][col];
+                *reinterpret_cast<float4 *>(to) = make_float4(g[0], g[1], g[2], g[3]);
+                *reinterpret_cast<float4 *>(to + 4) = make_float4(g[4], g[5], g[6], g[7]);
+            }
+        };
+        const int last = ts + (tiles - 1) * kBack;
+        Fetched done, now, next, then;  // as in the forward
+        fetch(last, now);
+        if (tiles > 1) fetch(last - kBack, next);
+        stage(last, 0, now);
+        __syncthreads();
+        for (int i = 0; i <= tiles; ++i) {
+            if (i + 2 < tiles) fetch(last - (i + 2) * kBack, then);
+            const int tp = last - (i - 1) * kBack, pb = (i - 1) & 1;  // the tile to finish
+            if (!kSum && i > 0) {
+#pragma unroll
+                for (int j = 0; j < kNI; ++j) {
+                    const int v = ht + j * kThreads;
+                    if (v >= 2 * kPer || tp + row >= te || nv <= 0) continue;
+                    const long long at = own + (long long)(tp + row) * p.D;
+                    f32x2 xv[4], g[4], o[4];
+                    get8(done.x[j], xv);
+                    get8(done.g[j], g);
+                    if (v < kPer) {
+                        f32x2 dd[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int e0 = c + ((2 * k) ^ key), e1 = c + ((2 * k + 1) ^ key);
+                            const float4 in = *reinterpret_cast<const float4 *>(&sm.in[pb][row][c + ((2 * k) ^ key2)]);
+                            const float2 u2 = *reinterpret_cast<const float2 *>(&sm.du[pb][row][c + 2 * k]);
+                            const f32x2 st = mk2(in.x, in.z), du = mk2(u2.x, u2.y);
+                            const auto &eb = sm.eb[kSum ? 0 : pb][row];
+                            const auto &fa = sm.fa[kSum ? 0 : pb][row];
+                            const f32x2 ev = mk2(lane_sum<kL>(eb[e0]), lane_sum<kL>(eb[e1]));
+                            o[k] = fma2(st, ev, mul2(skip[k], du));
+                            dd[k] = fma2(xv[k], ev, mk2(lane_sum<kL>(fa[e0]), lane_sum<kL>(fa[e1])));
+                            if (p.softplus) dd[k] = mul2(dd[k], sigmoid2(add2(g[k], bias[k])));
+                            gskip[k] = fma2(du, xv[k], gskip[k]);
+                            gbias[k] = add2(gbias[k], dd[k]);
+                        }
+                        put8<T, kVec>(static_cast<T *>(p.dx) + at, o, nv);
+                        put8<T, kVec>(static_cast<T *>(p.ddt) + at, dd, nv);
+                    } else if (z) {
+                        f32x2 zv[4];
+                        get8(done.z[j], zv);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const auto &up = sm.u[kSum ? 0 : pb][row];
+                            const f32x2 u = fma2(skip[k], xv[k], mk2(lane_sum<kL>(up[c + ((2 * k) ^ key)]), lane_sum<kL>(up[c + ((2 * k + 1) ^ key)])));
+                            const f32x2 sg = sigmoid2(zv[k]);  // silu' = sg (1 + z (1 - sg))
+                            const f32x2 ds = mul2(sg, fma2(zv[k], fma2(sg, dup(-1.f), dup(1.f)), dup(1.f)));
+                            o[k] = mul2(g[k], mul2(u, ds));
+                        }
+                        put8<T, kVec>(static_cast<T *>(p.dz) + at, o, nv);
+                    }
+                }
+                for (int j = ht; j < 2 * kBack * kN / 4; j += kThreads) {  // the warps' channels, in order
+                    const bool is_c = j >= kBack * kN / 4;
+                    const int r = j % (kBack * kN / 4), rr = r / (kN / 4), col = (r % (kN / 4)) * 4;
+                    if (tp + rr >= te) continue;
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < S::kParts; ++k) {
+                        const float4 v = *reinterpret_cast<const float4 *>(is_c ? &sm.dC[kSum ? 0 : pb][rr][k][col] : &sm.dB[kSum ? 0 : pb][rr][k][col]);
+                        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+                    }
+                    float *to = (is_c ? p.pC : p.pB) + (((long long)w.gt * p.B + b) * p.T + tp + rr) * kN + col;
+                    *reinterpret_cast<float4 *>(to) = a;
+                }
+                // other threads' elements of this tile are read above (du) before the next tile takes their place
+                asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+            }
+            if (i + 1 < tiles) stage(last - (i + 1) * kBack, (i + 1) & 1, next);
+            done = now;
+            now = next;
+            next = then;
+            if (i < tiles) __syncthreads();
+        }
+        if (kSum) return;
+        // dskip and ddt_bias: the tile rows' sums, in order (only the helpers are left)
+    float *acc = &sm.eb[0][0][0][0];  // [2][kBack][kCh], one buffer of parts
+        if (ht < kPer) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;
+                un2(gskip[k], lo, hi);
+                *reinterpret_cast<float2 *>(&acc[row * kCh + c + 2 * k]) = make_float2(lo, hi);
+                un2(gbias[k], lo, hi);
+                *reinterpret_cast<float2 *>(&acc[(kBack + row) * kCh + c + 2 * k]) = make_float2(lo, hi);
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+        for (int i = ht; i < 2 * kCh; i += kThreads) {
+            const int which = i / kCh, cc = i % kCh;
+            if (cc >= w.nch) continue;
+            float a = 0.f;
+            for (int k = 0; k < kBack; ++k) a += acc[(which * kBack + k) * kCh + cc];
+            p.pD[(srow * 2 + which) * p.D + w.c0 + cc] = a;
+        }
+        return;
     }
-    __syncthreads();  // the first tile is staged with them
+
+    // ---- the scan
+    const int sbase = p.seqs.cu ? 0 : b, warp = threadIdx.x / 32, cw = threadIdx.x % W::kC;  // cw: channel of the warp
+    const int part = warp * (S::kC / S::kFold) + cw / S::kFold;             // whose sums of dB and dC this lane has
+    const int at = w.n0 + (S::kFold == 2 ? 2 * (cw & 1) : cw & 3);          // and of which state
     State A;
     const State A2 = load_A2<kL>(p, w, &A);
     const long long ck0 = (long long)b * ((p.T + kBack - 1) / kBack);
@@ -372,80 +654,17 @@ __global__ void __launch_bounds__(kThreads) k_ssm_bwd(const SsmP p) {
     if (s1 <= te) e = end_grad(n);
     else e = kSum ? zero_state() : chain<kL>(p, w, A2, b, min((s1 - 1) / p.seg_len, p.S - 1), seg, -1);
     if (!kSum && te == p.T && p.seqs.cu && p.dh0)
-        for (int m = n + 1; m < p.seqs.n; ++m) pass_state<kL>(p, w, p.dht, p.dh0, m);
+        for (int j = n + 1; j < p.seqs.n; ++j) pass_state<kL>(p, w, p.dht, p.dh0, j);
     float total = 0.f;
     State gA = zero_state();
-    float gskip[8], gbias[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) gskip[i] = gbias[i] = 0.f;
-
-    Raw8<T> r1[kNV], r2[kNV], rb[kNB];
-    auto fetch = [&](int tb) {
-#pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            const int v = tid + i * kThreads, r = v % kVecs, row = tb + r / (kCh / 8), col = (r % (kCh / 8)) * 8;
-            const int nv = v < 2 * kVecs && row < te ? min(8, w.nch - col) : 0;
-            if (v < kVecs) {
-                r1[i] = load8<T, kVec>(x + row * p.x_row + col, nv);
-                r2[i] = load8<T, kVec>(dt + row * p.dt_row + col, nv);
-            } else {
-                r1[i] = load8<T, kVec>(dy + (long long)row * p.D + col, nv);
-                if (z) r2[i] = load8<T, kVec>(z + row * p.z_row + col, nv);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kNB; ++i) {
-            const int v = tid + i * kThreads, r = v % kBV, row = tb + r / (kN / 8), col = (r % (kN / 8)) * 8;
-            rb[i] = load8<T, kVec>(v >= kBV ? Cm + row * p.c_row + col : Bm + row * p.b_row + col,
-                                   v < 2 * kBV && row < te ? 8 : 0);
-        }
-    };
-    const int last = ts + (te - ts - 1) / kBack * kBack;
-    fetch(last);
+    const int last = ts + (tiles - 1) * kBack;
     State ck_next = zero_state();
     if (!kSum && w.on) ck_next = load_state(p.states + w.at(ck0 + last / kBack, p));
-    for (int tb = last; tb >= ts; tb -= kBack) {
-        Raw8<T> c1[kNV], c2[kNV];
-#pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            const int v = tid + i * kThreads, r = v % kVecs, row = r / (kCh / 8), col = (r % (kCh / 8)) * 8;
-            c1[i] = r1[i];
-            c2[i] = r2[i];
-            if (v >= 2 * kVecs) continue;
-            const bool real = tb + row < te;  // a row past the end changes nothing: s = 0, du = 0
-            float f1[8], f2[8];
-            unpack8(r1[i], f1);
-            unpack8(r2[i], f2);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float4 *to = &s_in[row][col + k];
-                if (v < kVecs) {
-                    const float raw = f2[k] + s_bias[col + k];
-                    const float s = !real ? 0.f : p.softplus ? softplusf(raw) : raw;
-                    to->x = s;
-                    to->y = s * f1[k];
-                    to->w = f1[k];
-                } else {
-                    to->z = z ? f1[k] * f2[k] * sigmoidf(f2[k]) : f1[k];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kNB; ++i) {
-            const int v = tid + i * kThreads, r = v % kBV, row = r / (kN / 8), col = (r % (kN / 8)) * 8;
-            if (v >= 2 * kBV) continue;
-            float f[8];
-            unpack8(rb[i], f);
-            float *to = v >= kBV ? &s_C[row][col] : &s_B[row][col];
-            *reinterpret_cast<float4 *>(to) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4 *>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        }
-        __syncthreads();
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        const int tb = last - i * kBack, buf = i & 1;
         const State ck = ck_next;
-        if (tb - kBack >= ts) {
-            fetch(tb - kBack);
-            if (!kSum && w.on) ck_next = load_state(p.states + w.at(ck0 + tb / kBack - 1, p));
-        }
+        if (!kSum && i + 1 < tiles && w.on) ck_next = load_state(p.states + w.at(ck0 + tb / kBack - 1, p));
         auto turn = [&](int t) {  // token t opens sequence n: e is its start state's gradient
             if (!kSum && p.dh0 && w.on) store_state(p.dh0 + w.at(sbase + n, p), e);
             e = zero_state();
@@ -459,156 +678,121 @@ __global__ void __launch_bounds__(kThreads) k_ssm_bwd(const SsmP p) {
             }
             if (s0 < t) e = end_grad(n);
         };
+        const int end = min(kBack, te - tb);
+        const bool opening = s0 > tb && s0 < tb + end;  // a sequence opens after the tile's first token
         if (kSum) {
-            for (int i = min(kBack, te - tb) - 1; i >= 0; --i) {
-                const float4 in = s_in[i][w.ch];
-                const State C = load_state(&s_C[i][w.n0]), a = decay(A2, in.x);
-                const f32x2 du = mk2(in.z, in.z);
-                e = State{mul2(a.a, fma2(du, C.a, e.a)), mul2(a.b, fma2(du, C.b, e.b))};
+            auto token = [&](int r) {
+                const float2 in = sm.in[buf][r][pair_place<kCh>(r, w.ch)];
+                const State C = load_state(&sm.C[buf][r][w.n0]), a = decay(A2, dup(in.x));
+                const f32x2 d2 = dup(sm.du[buf][r][w.ch]);
+                e = State{mul2(a.a, fma2(d2, C.a, e.a)), mul2(a.b, fma2(d2, C.b, e.b))};
                 total += in.x;
-                if (tb + i == s0) turn(tb + i);
+            };
+            if (opening) {
+                for (int r = end - 1; r >= 0; --r) {
+                    token(r);
+                    if (tb + r == s0) turn(tb + r);
+                }
+            } else {
+#pragma unroll
+                for (int r = kBack - 1; r >= 0; --r) token(r);
+                if (tb == s0) turn(tb);
             }
             __syncthreads();
             continue;
         }
-        State H[kBack], E[kBack];
-        {
-            int m = 0, next = p.T;  // the next sequence to open inside the tile
-            if (p.seqs.cu) {
-                m = p.seqs.find(tb);
-                next = p.seqs.bound(m + 1);
-            }
-            State h = ck;
-            float u[kL], v[kC][4];
+        State H[kBack];
+        State A2r = A2;  // opaque, or the compiler keeps the forward's decays (and spills them)
+        asm volatile("" : "+l"(A2r.a), "+l"(A2r.b));
+        // Tokens lo .. hi - 1 of the tile, all of one sequence, from state h.
+        // kPart: the others change nothing (s = 0, du = 0) and leave no result.
+        auto tile = [&](auto some, State h, int lo, int hi) {
+            constexpr bool kPart = decltype(some)::value;
+            const State hs = h;
+            auto mine = [&](int r) { return !kPart || (r >= lo && r < hi); };
+            auto factors = [&](int r, f32x2 &s2, f32x2 &i2, f32x2 &d2) {
+                const float2 in = sm.in[buf][r][pair_place<kCh>(r, w.ch)];
+                const float du = sm.du[buf][r][w.ch];
+                s2 = dup(mine(r) ? in.x : 0.f);
+                i2 = dup(mine(r) ? in.y : 0.f);
+                d2 = dup(mine(r) ? du : 0.f);
+            };
+            // Results are stored a group of tokens at a time: a store would
+            // hold back the loads behind it.
 #pragma unroll
-            for (int i = 0; i < kBack; ++i) {
-                if (p.seqs.cu && tb + i >= next && tb + i < te) {
-                    while (next <= tb + i && m + 1 < p.seqs.n) next = p.seqs.bound(++m + 1);
-                    h = start_state<kL>(p, w, m);
-                    if (next <= tb + i) next = p.T;
-                }
-                const float4 in = s_in[i][w.ch];
-                E[i] = decay(A2, in.x);
-                h = advance(E[i], h, in.y, load_state(&s_B[i][w.n0]));
-                H[i] = h;
-                if (z) {
-                    u[i % kL] = dot(h, load_state(&s_C[i][w.n0]));
-                    if (i % kL == kL - 1) s_u[kSum ? 0 : i - kL + 1 + w.q][w.ch] = lane_sums<kL>(u, w.q);
-                }
-                const f32x2 du = mk2(in.z, in.z);
-                un2(mul2(du, h.a), v[i % kC][0], v[i % kC][1]);
-                un2(mul2(du, h.b), v[i % kC][2], v[i % kC][3]);
-                if (i % kC == kC - 1) {
-                    channel_sums<kL, kC>(v, cw);
-                    *reinterpret_cast<float4 *>(&s_dC[kSum ? 0 : warp][i - kC + 1 + cw][w.n0]) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
-                }
-            }
-        }
-        {
-            float ub[kL], ua[kL], v[kC][4];
+            for (int g = 0; g < kBack; g += kGroup) {
+                float u[kGroup];
+                float2 c[kGroup];
 #pragma unroll
-            for (int i = kBack - 1; i >= 0; --i) {
-                const float4 in = s_in[i][w.ch];
-                const State C = load_state(&s_C[i][w.n0]), Bt = load_state(&s_B[i][w.n0]);
-                const bool opens = tb + i == s0 && tb + i < te;
-                const f32x2 du = mk2(in.z, in.z), sx = mk2(in.y, in.y), s2 = mk2(in.x, in.x);
-                e = State{fma2(du, C.a, e.a), fma2(du, C.b, e.b)};
-                ub[i % kL] = dot(e, Bt);
-                un2(mul2(e.a, sx), v[i % kC][0], v[i % kC][1]);
-                un2(mul2(e.b, sx), v[i % kC][2], v[i % kC][3]);
-                State before = i ? H[i ? i - 1 : 0] : ck;
-                if (opens && i) before = start_state<kL>(p, w, sbase + n);
-                e = State{mul2(e.a, E[i].a), mul2(e.b, E[i].b)};
-                const State f = State{mul2(e.a, before.a), mul2(e.b, before.b)};
-                ua[i % kL] = dot(f, A);
-                gA = State{fma2(f.a, s2, gA.a), fma2(f.b, s2, gA.b)};
-                if (opens) turn(tb + i);
-                if (i % kL == 0) {
-                    s_eb[kSum ? 0 : i + w.q][w.ch] = lane_sums<kL>(ub, w.q);
-                    s_fa[kSum ? 0 : i + w.q][w.ch] = lane_sums<kL>(ua, w.q);
+                for (int k = 0; k < kGroup; ++k) {
+                    const int r = g + k;
+                    f32x2 s2, i2, d2;
+                    factors(r, s2, i2, d2);
+                    h = advance(decay(A2, s2), h, i2, load_state(&sm.B[buf][r][w.n0]));
+                    H[r] = h;
+                    u[k] = dot(h, load_state(&sm.C[buf][r][w.n0]));
+                    c[k] = fold_channels<kL>(State{mul2(d2, h.a), mul2(d2, h.b)});
                 }
-                if (i % kC == 0) {
-                    channel_sums<kL, kC>(v, cw);
-                    *reinterpret_cast<float4 *>(&s_dB[kSum ? 0 : warp][i + cw][w.n0]) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    if (!mine(g + k)) continue;
+                    sm.u[kSum ? 0 : buf][g + k][place<kCh>(g + k, w.ch)][w.q] = u[k];
+                    put_fold<kL>(&sm.dC[kSum ? 0 : buf][g + k][part][at], c[k]);
                 }
             }
-        }
-        __syncthreads();
+            asm volatile("" ::: "memory");  // read the factors again rather than keep (and spill) sixteen tokens'
 #pragma unroll
-        for (int i = 0; i < kNV; ++i) {
-            const int v = tid + i * kThreads, r = v % kVecs, row = r / (kCh / 8), col = (r % (kCh / 8)) * 8;
-            if (v >= 2 * kVecs || tb + row >= te || col >= w.nch) continue;
-            const int nv = min(8, w.nch - col);
-            const long long at = own + (long long)(tb + row) * p.D + col;
-            float f1[8], f2[8], o1[8], o2[8];
-            unpack8(c1[i], f1);
-            unpack8(c2[i], f2);
+            for (int g = kBack - kGroup; g >= 0; g -= kGroup) {
+                float eb[kGroup], fa[kGroup];
+                float2 c[kGroup];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float4 in = s_in[row][col + k];
-                const float sk = s_skip[col + k];
-                if (v < kVecs) {
-                    const float eb = s_eb[kSum ? 0 : row][col + k];
-                    o1[k] = fmaf(in.x, eb, sk * in.z);
-                    o2[k] = fmaf(in.w, eb, s_fa[kSum ? 0 : row][col + k]);
-                    if (p.softplus) o2[k] *= sigmoidf(f2[k] + s_bias[col + k]);
-                    gskip[k] = fmaf(in.z, in.w, gskip[k]);
-                    gbias[k] += o2[k];
-                } else {
-                    const float g = sigmoidf(f2[k]), u = fmaf(sk, in.w, s_u[kSum ? 0 : row][col + k]);
-                    o1[k] = f1[k] * u * g * fmaf(f2[k], 1.f - g, 1.f);
+                for (int k = kGroup - 1; k >= 0; --k) {
+                    const int r = g + k;
+                    f32x2 s2, i2, d2;
+                    factors(r, s2, i2, d2);
+                    const State C = load_state(&sm.C[buf][r][w.n0]), Bt = load_state(&sm.B[buf][r][w.n0]);
+                    e = State{fma2(d2, C.a, e.a), fma2(d2, C.b, e.b)};
+                    eb[k] = dot(e, Bt);
+                    c[k] = fold_channels<kL>(State{mul2(i2, e.a), mul2(i2, e.b)});
+                    const State before = r ? H[r ? r - 1 : 0] : hs, E = decay(A2r, s2);
+                    e = State{mul2(e.a, E.a), mul2(e.b, E.b)};
+                    const State f = State{mul2(e.a, before.a), mul2(e.b, before.b)};
+                    fa[k] = dot(f, A);
+                    gA = State{fma2(f.a, s2, gA.a), fma2(f.b, s2, gA.b)};
+                }
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    if (!mine(g + k)) continue;
+                    const int e = place<kCh>(g + k, w.ch);
+                    sm.eb[kSum ? 0 : buf][g + k][e][w.q] = eb[k];
+                    sm.fa[kSum ? 0 : buf][g + k][e][w.q] = fa[k];
+                    put_fold<kL>(&sm.dB[kSum ? 0 : buf][g + k][part][at], c[k]);
                 }
             }
-            if (v < kVecs) {
-                store8<T, kVec>(static_cast<T *>(p.dx) + at, o1, nv);
-                store8<T, kVec>(static_cast<T *>(p.ddt) + at, o2, nv);
-            } else if (z) {
-                store8<T, kVec>(static_cast<T *>(p.dz) + at, o1, nv);
+        };
+        if (!opening) {
+            tile(std::false_type{}, ck, 0, kBack);
+            if (tb == s0) turn(tb);
+        } else {
+            for (int hi = end; hi > 0;) {  // the sequences in the tile, from the last
+                const int lo = max(s0 - tb, 0);
+                if (lo >= hi) break;
+                tile(std::true_type{}, lo ? start_state<kL>(p, w, sbase + n) : ck, lo, hi);
+                if (tb + lo != s0) break;
+                turn(s0);
+                hi = lo;
             }
-        }
-        for (int i = tid; i < 2 * kBack * kN / 4; i += kThreads) {  // the warps' channels, in order
-            const bool is_c = i >= kBack * kN / 4;
-            const int r = i % (kBack * kN / 4), row = r / (kN / 4), col = (r % (kN / 4)) * 4;
-            if (tb + row >= te) continue;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float4 v = *reinterpret_cast<const float4 *>(is_c ? &s_dC[kSum ? 0 : k][row][col] : &s_dB[kSum ? 0 : k][row][col]);
-                a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-            }
-            float *to = (is_c ? p.pC : p.pB) + (((long long)w.gt * p.B + b) * p.T + tb + row) * kN + col;
-            *reinterpret_cast<float4 *>(to) = a;
         }
         __syncthreads();
     }
-    const long long row = (long long)b * p.S + seg;
     if (kSum) {
         if (w.on) {
-            store_state(p.sum_h + w.at(row, p), e);
-            if (w.q == 0) p.sum_s[row * p.D + w.d] = total;
+            store_state(p.sum_h + w.at(srow, p), e);
+            if (w.q == 0) p.sum_s[srow * p.D + w.d] = total;
         }
         return;
     }
-    if (w.on) store_state(p.pA + w.at(row, p), gA);
-    // dskip and ddt_bias: the tile rows' sums, in order
-    float *acc = &s_in[0][0].x;  // [2][kBack][kCh]
-    static_assert(sizeof(s_in) >= 2 * kBack * kCh * sizeof(float), "");
-    if (tid < kVecs) {
-        const int rr = tid / (kCh / 8), col = (tid % (kCh / 8)) * 8;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            acc[rr * kCh + col + k] = gskip[k];
-            acc[(kBack + rr) * kCh + col + k] = gbias[k];
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < 2 * kCh; i += kThreads) {
-        const int which = i / kCh, c = i % kCh;
-        if (c >= w.nch) continue;
-        float a = 0.f;
-        for (int k = 0; k < kBack; ++k) a += acc[(which * kBack + k) * kCh + c];
-        p.pD[(row * 2 + which) * p.D + w.c0 + c] = a;
-    }
+    if (w.on) store_state(p.pA + w.at(srow, p), gA);
 }
 
 // Adds the partial gradients in order: dB and dC over a group's channel tiles,
@@ -680,7 +864,7 @@ __global__ void __launch_bounds__(kThreads) k_ssm_step(const StepP p) {
         const float raw = to_f(static_cast<const T *>(p.dt)[r * p.dt_row + d]) + (p.dt_bias ? p.dt_bias[d] : 0.f);
         const float s = p.softplus ? softplusf(raw) : raw;
         const f32x2 k = mk2(kLog2e, kLog2e);
-        const State h = advance(decay(State{mul2(A.a, k), mul2(A.b, k)}, s), h0, s * xv, Bt);
+        const State h = advance(decay(State{mul2(A.a, k), mul2(A.b, k)}, dup(s)), h0, dup(s * xv), Bt);
         store_state(st, h);
         u = dot(h, Ct);
     }
@@ -764,13 +948,16 @@ SsmSpace ssm_space(const gdr_ssm_args *a, const SsmPlan &pl, bool bwd) {
     return s;
 }
 
+// Whether eight channels are always there and 16-byte aligned.
 bool ssm_vec(const gdr_ssm_args *a) {
     const long long q = a->dtype == GDR_BF16 ? 8 : 4;
     for (long long v : {a->x_row, a->x_batch, a->dt_row, a->dt_batch, a->z ? a->z_row : 0, a->z ? a->z_batch : 0,
                         a->b_row, a->b_batch, a->c_row, a->c_batch})
         if (v % q) return false;
-    return (a->D / a->G) % 8 == 0 && multiple16(a->x) && multiple16(a->dt) && multiple16(a->z) && multiple16(a->Bm) &&
-           multiple16(a->Cm);
+    for (const void *p : {a->x, a->dt, a->z, a->Bm, a->Cm, a->dy, static_cast<const void *>(a->y), static_cast<const void *>(a->dx),
+                          static_cast<const void *>(a->ddt), static_cast<const void *>(a->dz)})
+        if (!multiple16(p)) return false;
+    return (a->D / a->G) % 8 == 0;
 }
 
 int ssm_common(const gdr_ssm_args *a, Seqs *s) {
@@ -834,6 +1021,14 @@ int ssm_workspace(const gdr_ssm_args *a, size_t need, const char *what) {
     return GDR_OK;
 }
 
+template <typename K>
+int ssm_launch(K *kernel, size_t smem, dim3 grid, const SsmP &p, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return layer_fail(GDR_ERR_CUDA, "scan: %s", cudaGetErrorString(e));
+    kernel<<<grid, 2 * kThreads, smem, st>>>(p);
+    return GDR_OK;
+}
+
 // A call without tokens hands the states through.
 int ssm_hand_on(const float *from, float *to, size_t n, cudaStream_t st) {
     if (!to) return GDR_OK;
@@ -879,16 +1074,17 @@ int gdr_ssm_fwd(const gdr_ssm_args *a, void *stream) {
     if ((rc = ssm_workspace(a, sp.total, "scan forward"))) return rc;
     SsmP p;
     ssm_fill(a, s, pl, sp, &p);
-    const bool vec = ssm_vec(a) && multiple16(a->y);
+    const bool vec = ssm_vec(a);
     ssm_by_type(a->dtype, a->N, vec, [&](auto t, auto l, auto v) {
         using E = decltype(t);
         constexpr int L = decltype(l)::value;
         constexpr bool V = decltype(v)::value;
         const unsigned gx = (unsigned)(pl.tiles * a->G), gz = (unsigned)a->B;
-        if (pl.S > 1) k_ssm_fwd<E, L, V, true><<<dim3(gx, pl.S - 1, gz), kThreads, 0, st>>>(p);
-        k_ssm_fwd<E, L, V, false><<<dim3(gx, pl.S, gz), kThreads, 0, st>>>(p);
+        rc = GDR_OK;
+        if (pl.S > 1) rc = ssm_launch(k_ssm_fwd<E, L, V, true>, sizeof(FwdSmem<L, true>), dim3(gx, pl.S - 1, gz), p, st);
+        if (!rc) rc = ssm_launch(k_ssm_fwd<E, L, V, false>, sizeof(FwdSmem<L, false>), dim3(gx, pl.S, gz), p, st);
     });
-    return layer_launched("scan forward");
+    return rc ? rc : layer_launched("scan forward");
 }
 
 int gdr_ssm_bwd(const gdr_ssm_args *a, void *stream) {
@@ -916,18 +1112,19 @@ int gdr_ssm_bwd(const gdr_ssm_args *a, void *stream) {
     if ((rc = ssm_workspace(a, sp.total, "scan backward"))) return rc;
     SsmP p;
     ssm_fill(a, s, pl, sp, &p);
-    const bool vec = ssm_vec(a) && multiple16(a->dy) && multiple16(a->dx) && multiple16(a->ddt) && multiple16(a->dz);
+    const bool vec = ssm_vec(a);
     const long long outs = 2 * a->B * a->T * a->G * a->N + a->D * a->N + 2 * a->D;
     ssm_by_type(a->dtype, a->N, vec, [&](auto t, auto l, auto v) {
         using E = decltype(t);
         constexpr int L = decltype(l)::value;
         constexpr bool V = decltype(v)::value;
         const unsigned gx = (unsigned)(pl.tiles * a->G), gz = (unsigned)a->B;
-        if (pl.S > 1) k_ssm_bwd<E, L, V, true><<<dim3(gx, pl.S - 1, gz), kThreads, 0, st>>>(p);
-        k_ssm_bwd<E, L, V, false><<<dim3(gx, pl.S, gz), kThreads, 0, st>>>(p);
-        k_ssm_bwd_sum<E><<<(unsigned)((outs + 255) / 256), 256, 0, st>>>(p, a->N);
+        rc = GDR_OK;
+        if (pl.S > 1) rc = ssm_launch(k_ssm_bwd<E, L, V, true>, sizeof(BwdSmem<L, true>), dim3(gx, pl.S - 1, gz), p, st);
+        if (!rc) rc = ssm_launch(k_ssm_bwd<E, L, V, false>, sizeof(BwdSmem<L, false>), dim3(gx, pl.S, gz), p, st);
+        if (!rc) k_ssm_bwd_sum<E><<<(unsigned)((outs + 255) / 256), 256, 0, st>>>(p, a->N);
     });
-    return layer_launched("scan backward");
+    return rc ? rc : layer_launched("scan backward");
 }
 
 int gdr_ssm_step(const gdr_ssm_step_args *a, void *stream) {

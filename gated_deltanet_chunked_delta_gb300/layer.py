@@ -21,10 +21,10 @@ current stream of the inputs' device; nothing synchronises.
 from __future__ import annotations
 
 import ctypes
+import struct
 from ctypes import c_float, c_int, c_longlong, c_size_t, c_void_p
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from .binding import GDR_BF16, GDR_F32, GdrError, load
 
@@ -35,32 +35,41 @@ STATE_STRIDE = 16  # GDR_SSM_STRIDE: tokens between the states kept for the back
 STATE_SIZES = (8, 16, 32, 64)
 
 _DTYPES = {torch.bfloat16: GDR_BF16, torch.float32: GDR_F32}
-_F32 = torch.float32
+_F32, _I32 = torch.float32, torch.int32
+_empty = torch.empty
 
 
-def _struct(name, spec):
-    kinds = {"p": c_void_p, "l": c_longlong, "i": c_int, "f": c_float, "z": c_size_t}
-    fields = [(n, kinds[k]) for k, names in spec for n in names.split()]
-    return type(name, (ctypes.Structure,), {"_fields_": fields})
+class _Args:
+    """An argument struct of the C ABI: its ctypes class, and ``pack``, which lays all of its fields out at once
+    (a call for one token is bound by the host; filling a ctypes structure takes twice as long)."""
+
+    def __init__(self, name, spec):
+        kinds = {"p": (c_void_p, "P"), "l": (c_longlong, "q"), "i": (c_int, "i"), "f": (c_float, "f"), "z": (c_size_t, "N")}
+        fields = [(n, kinds[k]) for k, names in spec for n in names.split()]
+        self.struct = type(name, (ctypes.Structure,), {"_fields_": [(n, k[0]) for n, k in fields]})
+        form = struct.Struct("@" + "".join(k[1] for _, k in fields))
+        self.pack = form.pack
 
 
-_ConvArgs = _struct("gdr_conv_args", [("p", "x weight bias h0 cu_seqlens"), ("l", "B T D n_seqs x_row x_batch"),
-                                      ("i", "W dtype silu"), ("p", "y ht dy dht dx dweight dbias dh0 workspace"),
-                                      ("z", "workspace_bytes")])
-_ConvStepArgs = _struct("gdr_conv_step_args", [("p", "x weight bias state slots"), ("l", "rows D n_slots x_row"),
-                                               ("i", "W dtype silu"), ("p", "y")])
-_SsmArgs = _struct("gdr_ssm_args", [
+_CONV = _Args("gdr_conv_args", [("p", "x weight bias h0 cu_seqlens"), ("l", "B T D n_seqs x_row x_batch"),
+                                ("i", "W dtype silu"), ("p", "y ht dy dht dx dweight dbias dh0 workspace"),
+                                ("z", "workspace_bytes")])
+_CONV_STEP = _Args("gdr_conv_step_args", [("p", "x weight bias state slots"), ("l", "rows D n_slots x_row"),
+                                          ("i", "W dtype silu"), ("p", "y")])
+_SSM = _Args("gdr_ssm_args", [
     ("p", "x dt z Bm Cm A skip dt_bias h0 cu_seqlens"), ("l", "B T D G n_seqs"),
     ("l", "x_row x_batch dt_row dt_batch z_row z_batch b_row b_batch c_row c_batch"), ("i", "N dtype softplus"),
     ("p", "y ht states dy dht dx ddt dz dB dC dA dskip ddt_bias dh0 workspace"), ("z", "workspace_bytes")])
-_SsmStepArgs = _struct("gdr_ssm_step_args", [
+_SSM_STEP = _Args("gdr_ssm_step_args", [
     ("p", "x dt z Bm Cm A skip dt_bias state slots"), ("l", "rows D G n_slots x_row dt_row z_row b_row c_row"),
     ("i", "N dtype softplus"), ("p", "y")])
-_NormArgs = _struct("gdr_norm_args", [("p", "x residual weight"), ("l", "M D x_row r_row"), ("f", "eps"), ("i", "dtype"),
-                                      ("p", "sum y q scales")])
-_NormBwdArgs = _struct("gdr_norm_bwd_args", [("p", "r dy dsum weight"), ("l", "M D"), ("f", "eps"), ("i", "dtype"),
-                                             ("p", "dr dweight workspace"), ("z", "workspace_bytes")])
-_Fp8Args = _struct("gdr_fp8_args", [("p", "a b a_scales b_scales"), ("l", "M N K"), ("i", "out_dtype"), ("p", "out")])
+_NORM = _Args("gdr_norm_args", [("p", "x residual weight"), ("l", "M D x_row r_row"), ("f", "eps"), ("i", "dtype"),
+                                ("p", "sum y q scales")])
+_NORM_BWD = _Args("gdr_norm_bwd_args", [("p", "r dy dsum weight"), ("l", "M D"), ("f", "eps"), ("i", "dtype"),
+                                        ("p", "dr dweight workspace"), ("z", "workspace_bytes")])
+_FP8 = _Args("gdr_fp8_args", [("p", "a b a_scales b_scales"), ("l", "M N K"), ("i", "out_dtype"), ("p", "out")])
+_ConvArgs, _ConvStepArgs, _SsmArgs, _SsmStepArgs, _NormArgs, _NormBwdArgs, _Fp8Args = (
+    v.struct for v in (_CONV, _CONV_STEP, _SSM, _SSM_STEP, _NORM, _NORM_BWD, _FP8))
 
 _lib = None
 
@@ -81,12 +90,17 @@ def _calls():
     return _lib
 
 
-def _run(call, args, device):
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            rc = call(ctypes.byref(args), torch.cuda.current_stream(device).cuda_stream)
+_current_device = torch.cuda.current_device
+# The current stream's handle without building a Stream object, where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _run(call, args, dev):
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            rc = call(args, _raw_stream(dev))
     else:
-        rc = call(ctypes.byref(args), torch.cuda.current_stream().cuda_stream)
+        rc = call(args, _raw_stream(dev))
     if rc:
         raise GdrError(rc, load().gdr_last_error().decode())
 
@@ -96,73 +110,85 @@ def _fail(code, msg):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _inputs(name, t, shape=None):
-    """An activation: its type's code, after the checks every operator makes."""
-    if not t.is_cuda:
+def _inputs(name, t):
+    """A call's first input: its GPU and its type's code."""
+    dev = t.get_device()
+    if dev < 0:
         _fail(1, f"{name} must live on the GPU")
     code = _DTYPES.get(t.dtype)
     if code is None:
         _fail(3, f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         _fail(1, f"{name} must be contiguous along its last dimension")
-    return code
+    return dev, code
 
 
-def _like(name, t, x, shape):
-    """Another activation of a call whose first is x."""
-    if t.device != x.device:
+def _like(name, t, dev, dtype, shape):
+    """Another activation of the call."""
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and (t.stride(-1) == 1 or t.shape[-1] <= 1):
+        return
+    if t.get_device() != dev:
         _fail(1, f"{name} must live on the GPU of the first input")
-    if t.dtype != x.dtype:
-        _fail(3, f"{name} must have the first input's dtype ({x.dtype}, got {t.dtype})")
+    if t.dtype != dtype:
+        _fail(3, f"{name} must have the first input's dtype ({dtype}, got {t.dtype})")
     if t.shape != shape:
         _fail(2, f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        _fail(1, f"{name} must be contiguous along its last dimension")
+    _fail(1, f"{name} must be contiguous along its last dimension")
 
 
-def _param(name, t, x, shape, dtype=_F32):
+def _param(name, t, dev, shape, dtype=_F32):
     """A parameter, state or table: contiguous, of one type and shape."""
-    if t.device != x.device:
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return
+    if t.get_device() != dev:
         _fail(1, f"{name} must live on the GPU of the first input")
     if t.dtype != dtype:
         _fail(3, f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         _fail(2, f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
-    if not t.is_contiguous():
-        _fail(1, f"{name} must be contiguous")
+    _fail(1, f"{name} must be contiguous")
 
 
-def _sequences(x, cu_seqlens):
+def _sequences(x, dev, cu_seqlens):
     if cu_seqlens is None:
         return x.shape[0]
-    if cu_seqlens.device != x.device or not cu_seqlens.is_contiguous():
+    if cu_seqlens.get_device() != dev or not cu_seqlens.is_contiguous():
         _fail(1, "cu_seqlens must be contiguous and live on the GPU of the first input")
-    if cu_seqlens.dtype != torch.int32:
+    if cu_seqlens.dtype != _I32:
         _fail(3, "cu_seqlens must be int32")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2 or x.shape[0] != 1:
         _fail(2, "packed sequences need B == 1 and cu_seqlens [n_seqs + 1]")
     return cu_seqlens.shape[0] - 1
 
 
-def _slots(slots, x, rows, n_slots):
+def _slots(slots, dev, rows, n_slots):
     if slots is not None:
-        _param("slots", slots, x, (rows,), torch.int32)
+        _param("slots", slots, dev, (rows,), _I32)
     elif n_slots < rows:
         _fail(2, f"{n_slots} state slots for {rows} rows")
 
 
 def _wants_grad(*ts):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def _grad(g, like):
     """An incoming gradient as the kernels read it."""
-    if g is None:
-        return None
+    if g is None or (g.dtype is like.dtype and g.is_contiguous()):
+        return g
     return g.to(like.dtype).contiguous()
+
+
+def _once():
+    if torch.is_grad_enabled():
+        _fail(1, "the gradient of this operator is not differentiable itself")
 
 
 # ---- short convolution ------------------------------------------------------
@@ -175,29 +201,30 @@ def _activation(activation):
 
 
 def _conv_check(x, weight, bias, initial_state, cu_seqlens):
-    code = _inputs("x", x)
+    dev, code = _inputs("x", x)
     if x.dim() != 3:
         _fail(2, f"x must be [B, T, D] (got {tuple(x.shape)})")
-    n, d = _sequences(x, cu_seqlens), x.shape[2]
+    n, d = _sequences(x, dev, cu_seqlens), x.shape[2]
     if weight.dim() != 2:
         _fail(2, f"weight must be [D, W] (got {tuple(weight.shape)})")
     w = weight.shape[1]
-    _param("weight", weight, x, (d, w))
+    _param("weight", weight, dev, (d, w))
     if bias is not None:
-        _param("bias", bias, x, (d,))
+        _param("bias", bias, dev, (d,))
     if initial_state is not None:
-        _param("initial_state", initial_state, x, (n, w - 1, d), x.dtype)
-    return code, n, w
+        _param("initial_state", initial_state, dev, (n, w - 1, d), x.dtype)
+    return dev, code, n, w
 
 
 def _conv_fwd(x, weight, bias, silu, initial_state, output_final_state, cu_seqlens):
-    code, n, w = _conv_check(x, weight, bias, initial_state, cu_seqlens)
+    dev, code, n, w = _conv_check(x, weight, bias, initial_state, cu_seqlens)
     b, t, d = x.shape
-    y = torch.empty((b, t, d), dtype=x.dtype, device=x.device)
-    ht = torch.empty((n, w - 1, d), dtype=x.dtype, device=x.device) if output_final_state and w > 1 else None
-    a = _ConvArgs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), b, t, d, n,
-                  x.stride(1), x.stride(0), w, code, silu, y.data_ptr(), _ptr(ht))
-    _run(_calls().gdr_conv_fwd, a, x.device)
+    y = _empty((b, t, d), dtype=x.dtype, device=x.device)
+    ht = _empty((n, w - 1, d), dtype=x.dtype, device=x.device) if output_final_state and w > 1 else None
+    row = x.stride()
+    _run(_calls().gdr_conv_fwd,
+         _CONV.pack(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), b, t, d, n, row[1],
+                    row[0], w, code, silu, y.data_ptr(), _ptr(ht), 0, 0, 0, 0, 0, 0, 0, 0), dev)
     return y, ht
 
 
@@ -210,24 +237,25 @@ class _ShortConv(torch.autograd.Function):
         return _conv_fwd(x, weight, bias, silu, initial_state, output_final_state, cu_seqlens)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dy, dht):
+        _once()
         x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
-        (b, t, d), w = x.shape, weight.shape[1]
+        (b, t, d), w, dev = x.shape, weight.shape[1], x.device
         n = b if cu_seqlens is None else cu_seqlens.shape[0] - 1
-        dy = torch.zeros((b, t, d), dtype=x.dtype, device=x.device) if dy is None else _grad(dy, x)
+        dy = torch.zeros((b, t, d), dtype=x.dtype, device=dev) if dy is None else _grad(dy, x)
         dht = _grad(dht, x)
-        dx = torch.empty((b, t, d), dtype=x.dtype, device=x.device)
-        dweight = torch.empty_like(weight)
-        dbias = None if bias is None else torch.empty_like(bias)
-        dh0 = None if initial_state is None else torch.empty_like(initial_state)
+        dx = _empty((b, t, d), dtype=x.dtype, device=dev)
+        dweight = _empty((d, w), dtype=_F32, device=dev)
+        dbias = None if bias is None else _empty((d,), dtype=_F32, device=dev)
+        dh0 = None if initial_state is None else _empty(initial_state.shape, dtype=x.dtype, device=dev)
         lib = _calls()
         size = lib.gdr_conv_bwd_workspace_size(b, t, d, w)
-        ws = torch.empty(size, dtype=torch.uint8, device=x.device)
-        a = _ConvArgs(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), b, t, d, n,
-                      x.stride(1), x.stride(0), w, _DTYPES[x.dtype], ctx.silu, None, None, dy.data_ptr(), _ptr(dht),
-                      dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), _ptr(dh0), ws.data_ptr(), size)
-        _run(lib.gdr_conv_bwd, a, x.device)
+        ws = _empty(size, dtype=torch.uint8, device=dev)
+        row = x.stride()
+        _run(lib.gdr_conv_bwd,
+             _CONV.pack(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), b, t, d, n, row[1],
+                        row[0], w, _DTYPES[x.dtype], ctx.silu, 0, 0, dy.data_ptr(), _ptr(dht), dx.data_ptr(),
+                        dweight.data_ptr(), _ptr(dbias), _ptr(dh0), ws.data_ptr(), size), x.get_device())
         return dx, dweight, dbias, None, dh0, None, None
 
 
@@ -248,21 +276,21 @@ def short_conv_step(x, weight, state, bias=None, activation="silu", slots=None):
     int32 names each row's state (row r uses slot r when absent), a negative one an idle row whose y is zero.
     Returns y [rows, D].  No gradient."""
     silu = _activation(activation)
-    code = _inputs("x", x)
+    dev, code = _inputs("x", x)
     if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
         _fail(2, "x must be [rows, D], weight [D, W] and state [n_slots, W - 1, D]")
     (rows, d), w, n = x.shape, weight.shape[1], state.shape[0]
-    _param("weight", weight, x, (d, w))
-    _param("state", state, x, (n, w - 1, d), x.dtype)
+    _param("weight", weight, dev, (d, w))
+    _param("state", state, dev, (n, w - 1, d), x.dtype)
     if bias is not None:
-        _param("bias", bias, x, (d,))
-    _slots(slots, x, rows, n)
+        _param("bias", bias, dev, (d,))
+    _slots(slots, dev, rows, n)
     if _wants_grad(x, weight, bias, state):
         _fail(1, "short_conv_step has no gradient: call it under torch.no_grad() or detach its inputs")
-    y = torch.empty((rows, d), dtype=x.dtype, device=x.device)
-    a = _ConvStepArgs(x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(), _ptr(slots), rows, d, n, x.stride(0),
-                      w, code, silu, y.data_ptr())
-    _run(_calls().gdr_conv_step, a, x.device)
+    y = _empty((rows, d), dtype=x.dtype, device=x.device)
+    _run(_calls().gdr_conv_step,
+         _CONV_STEP.pack(x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(), _ptr(slots), rows, d, n, x.stride(0),
+                         w, code, silu, y.data_ptr()), dev)
     return y
 
 
@@ -271,10 +299,11 @@ def short_conv_step(x, weight, state, bias=None, activation="silu", slots=None):
 
 def _ssm_check(x, dt, A, B, C, D, z, dt_bias, lead):
     """Shapes of the scan (lead 2: [B, T, ...]) and of its step (lead 1: [rows, ...])."""
-    code = _inputs("x", x)
-    if x.dim() != lead + 1:
-        _fail(2, f"x must be {'[B, T, D]' if lead == 2 else '[rows, D]'} (got {tuple(x.shape)})")
-    d = x.shape[-1]
+    dev, code = _inputs("x", x)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != lead + 1:
+        _fail(2, f"x must be {'[B, T, D]' if lead == 2 else '[rows, D]'} (got {tuple(shape)})")
+    d = shape[-1]
     if A.dim() != 2 or B.dim() != lead + 2:
         _fail(2, f"A must be [D, N] and B {'[B, T, G, N]' if lead == 2 else '[rows, G, N]'}")
     n, g = A.shape[1], B.shape[-2]
@@ -282,46 +311,47 @@ def _ssm_check(x, dt, A, B, C, D, z, dt_bias, lead):
         _fail(2, f"N must be one of {STATE_SIZES} (got {n})")
     if g < 1 or d % g:
         _fail(2, f"D ({d}) must be a multiple of G ({g})")
-    _param("A", A, x, (d, n))
-    _like("dt", dt, x, x.shape)
-    for name, t in (("B", B), ("C", C)):
-        _like(name, t, x, (*x.shape[:lead], g, n))
-        if g > 1 and t.stride(-2) != n:
-            _fail(1, f"{name} must be contiguous over its last two dimensions")
+    _param("A", A, dev, (d, n))
+    _like("dt", dt, dev, dtype, shape)
+    inner = (*shape[:lead], g, n)
+    _like("B", B, dev, dtype, inner)
+    _like("C", C, dev, dtype, inner)
+    if g > 1 and not B.stride(-2) == C.stride(-2) == n:
+        _fail(1, "B and C must be contiguous over their last two dimensions")
     if z is not None:
-        _like("z", z, x, x.shape)
+        _like("z", z, dev, dtype, shape)
     if D is not None:
-        _param("D", D, x, (d,))
+        _param("D", D, dev, (d,))
     if dt_bias is not None:
-        _param("dt_bias", dt_bias, x, (d,))
-    return code, d, n, g
+        _param("dt_bias", dt_bias, dev, (d,))
+    return dev, code, d, n, g
 
 
-def _ssm_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, cu_seqlens, n_seqs, code, out):
-    return _SsmArgs(x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D), _ptr(dt_bias),
-                    _ptr(initial_state), _ptr(cu_seqlens), x.shape[0], x.shape[1], x.shape[2], B.shape[2], n_seqs,
-                    x.stride(1), x.stride(0), dt.stride(1), dt.stride(0), 0 if z is None else z.stride(1),
-                    0 if z is None else z.stride(0), B.stride(1), B.stride(0), C.stride(1), C.stride(0),
-                    A.shape[1], code, softplus, *out)
+def _ssm_head(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, cu_seqlens, n_seqs, code):
+    """The first 28 fields of the scan's arguments: inputs, sizes, strides, kinds."""
+    b, t, d = x.shape
+    xs, ds, bs, cs = x.stride(), dt.stride(), B.stride(), C.stride()
+    zs = (0, 0) if z is None else z.stride()
+    return (x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D), _ptr(dt_bias),
+            _ptr(initial_state), _ptr(cu_seqlens), b, t, d, B.shape[2], n_seqs, xs[1], xs[0], ds[1], ds[0], zs[1], zs[0],
+            bs[1], bs[0], cs[1], cs[0], A.shape[1], code, softplus)
 
 
 def _scan_fwd(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, output_final_state, cu_seqlens, keep):
-    code, d, n, _ = _ssm_check(x, dt, A, B, C, D, z, dt_bias, 2)
-    n_seqs = _sequences(x, cu_seqlens)
+    dev, code, d, n, _ = _ssm_check(x, dt, A, B, C, D, z, dt_bias, 2)
+    n_seqs = _sequences(x, dev, cu_seqlens)
     if initial_state is not None:
-        _param("initial_state", initial_state, x, (n_seqs, d, n))
-    b, t, dev = x.shape[0], x.shape[1], x.device
-    y = torch.empty((b, t, d), dtype=x.dtype, device=dev)
-    ht = torch.empty((n_seqs, d, n), dtype=_F32, device=dev) if output_final_state else None
-    states = torch.empty((b, -(-t // STATE_STRIDE), d, n), dtype=_F32, device=dev) if keep else None
-    a = _ssm_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, cu_seqlens, n_seqs, code,
-                  (y.data_ptr(), _ptr(ht), _ptr(states)))
+        _param("initial_state", initial_state, dev, (n_seqs, d, n))
+    b, t, where = x.shape[0], x.shape[1], x.device
+    y = _empty((b, t, d), dtype=x.dtype, device=where)
+    ht = _empty((n_seqs, d, n), dtype=_F32, device=where) if output_final_state else None
+    states = _empty((b, -(-t // STATE_STRIDE), d, n), dtype=_F32, device=where) if keep else None
+    head = _ssm_head(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, cu_seqlens, n_seqs, code)
+    out = (y.data_ptr(), _ptr(ht), _ptr(states), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     lib = _calls()
-    size = lib.gdr_ssm_fwd_workspace_size(ctypes.byref(a))
-    if size:
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), size
-    _run(lib.gdr_ssm_fwd, a, dev)
+    size = lib.gdr_ssm_fwd_workspace_size(_SSM.pack(*head, *out, 0, 0))
+    ws = _empty(size, dtype=torch.uint8, device=where) if size else None
+    _run(lib.gdr_ssm_fwd, _SSM.pack(*head, *out, _ptr(ws), size), dev)
     return y, ht, states
 
 
@@ -336,24 +366,22 @@ class _StateSpaceScan(torch.autograd.Function):
         return y, ht
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dy, dht):
+        _once()
         x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, states = ctx.saved_tensors
-        b, t, d = x.shape
-        n_seqs = b if cu_seqlens is None else cu_seqlens.shape[0] - 1
-        dy = torch.zeros((b, t, d), dtype=x.dtype, device=x.device) if dy is None else _grad(dy, x)
+        where = x.device
+        n_seqs = x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=where) if dy is None else _grad(dy, x)
         dht = _grad(dht, A)
-        new = lambda like: None if like is None else torch.empty(like.shape, dtype=like.dtype, device=like.device)  # noqa: E731
+        new = lambda like: None if like is None else _empty(like.shape, dtype=like.dtype, device=where)  # noqa: E731
         dx, ddt, dA, dB, dC, dD, dz, db, dh0 = (new(v) for v in (x, dt, A, B, C, D, z, dt_bias, initial_state))
-        a = _ssm_args(x, dt, A, B, C, D, z, dt_bias, ctx.softplus, initial_state, cu_seqlens, n_seqs, _DTYPES[x.dtype],
-                      (None, None, states.data_ptr(), dy.data_ptr(), _ptr(dht), dx.data_ptr(), ddt.data_ptr(), _ptr(dz),
-                       dB.data_ptr(), dC.data_ptr(), dA.data_ptr(), _ptr(dD), _ptr(db), _ptr(dh0)))
+        head = _ssm_head(x, dt, A, B, C, D, z, dt_bias, ctx.softplus, initial_state, cu_seqlens, n_seqs, _DTYPES[x.dtype])
+        out = (0, 0, states.data_ptr(), dy.data_ptr(), _ptr(dht), dx.data_ptr(), ddt.data_ptr(), _ptr(dz), dB.data_ptr(),
+               dC.data_ptr(), dA.data_ptr(), _ptr(dD), _ptr(db), _ptr(dh0))
         lib = _calls()
-        size = lib.gdr_ssm_bwd_workspace_size(ctypes.byref(a))
-        if size:
-            ws = torch.empty(size, dtype=torch.uint8, device=x.device)
-            a.workspace, a.workspace_bytes = ws.data_ptr(), size
-        _run(lib.gdr_ssm_bwd, a, x.device)
+        size = lib.gdr_ssm_bwd_workspace_size(_SSM.pack(*head, *out, 0, 0))
+        ws = _empty(size, dtype=torch.uint8, device=where) if size else None
+        _run(lib.gdr_ssm_bwd, _SSM.pack(*head, *out, _ptr(ws), size), x.get_device())
         return dx, ddt, dA, dB, dC, dD, dz, db, None, dh0, None, None
 
 
@@ -377,18 +405,18 @@ def state_space_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=T
 def state_space_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus=True, slots=None):
     """One token of every row: x, dt, z [rows, D]; B, C [rows, G, N]; state [n_slots, D, N] fp32, updated in place;
     slots as in ``short_conv_step``.  Returns y [rows, D].  No gradient."""
-    code, d, n, g = _ssm_check(x, dt, A, B, C, D, z, dt_bias, 1)
+    dev, code, d, n, g = _ssm_check(x, dt, A, B, C, D, z, dt_bias, 1)
     rows, n_slots = x.shape[0], state.shape[0]
-    _param("state", state, x, (n_slots, d, n))
-    _slots(slots, x, rows, n_slots)
+    _param("state", state, dev, (n_slots, d, n))
+    _slots(slots, dev, rows, n_slots)
     if _wants_grad(x, dt, A, B, C, D, z, dt_bias, state):
         _fail(1, "state_space_step has no gradient: call it under torch.no_grad() or detach its inputs")
-    y = torch.empty((rows, d), dtype=x.dtype, device=x.device)
-    a = _SsmStepArgs(x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D), _ptr(dt_bias),
-                     state.data_ptr(), _ptr(slots), rows, d, g, n_slots, x.stride(0), dt.stride(0),
-                     0 if z is None else z.stride(0), B.stride(0), C.stride(0), n, code, 1 if dt_softplus else 0,
-                     y.data_ptr())
-    _run(_calls().gdr_ssm_step, a, x.device)
+    y = _empty((rows, d), dtype=x.dtype, device=x.device)
+    _run(_calls().gdr_ssm_step,
+         _SSM_STEP.pack(x.data_ptr(), dt.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _ptr(D), _ptr(dt_bias),
+                        state.data_ptr(), _ptr(slots), rows, d, g, n_slots, x.stride(0), dt.stride(0),
+                        0 if z is None else z.stride(0), B.stride(0), C.stride(0), n, code, 1 if dt_softplus else 0,
+                        y.data_ptr()), dev)
     return y
 
 
@@ -406,27 +434,29 @@ def _rows(name, t, d):
 
 
 def _norm_fwd(x, weight, residual, eps, quantise):
-    code = _inputs("x", x)
-    if x.dim() < 1 or x.shape[-1] < 1:
-        _fail(2, f"x must be [..., D] (got {tuple(x.shape)})")
-    d, dev = x.shape[-1], x.device
-    _param("weight", weight, x, (d,))
+    dev, code = _inputs("x", x)
+    shape, where = x.shape, x.device
+    if not shape or shape[-1] < 1:
+        _fail(2, f"x must be [..., D] (got {tuple(shape)})")
+    d = shape[-1]
+    _param("weight", weight, dev, (d,))
     x2 = _rows("x", x, d)
-    m, out, r2 = x2.shape[0], x, None
+    m, out, res, row = x2.shape[0], x, 0, 0
     if residual is not None:
-        _like("residual", residual, x, x.shape)
+        _like("residual", residual, dev, x.dtype, shape)
         r2 = _rows("residual", residual, d)
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    scales = None
+        res, row = r2.data_ptr(), r2.stride(0)
+        out = _empty(shape, dtype=x.dtype, device=where)
     if quantise:
-        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty((-(-d // 128), m), dtype=_F32, device=dev)
+        y = _empty(shape, dtype=torch.float8_e4m3fn, device=where)
+        scales = _empty((-(-d // 128), m), dtype=_F32, device=where)
+        to = (0, y.data_ptr(), scales.data_ptr())
     else:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    a = _NormArgs(x2.data_ptr(), _ptr(r2), weight.data_ptr(), m, d, x2.stride(0), 0 if r2 is None else r2.stride(0), eps, code,
-                  None if r2 is None else out.data_ptr(), None if quantise else y.data_ptr(),
-                  y.data_ptr() if quantise else None, _ptr(scales))
-    _run(_calls().gdr_norm_fwd, a, dev)
+        y, scales = _empty(shape, dtype=x.dtype, device=where), None
+        to = (y.data_ptr(), 0, 0)
+    _run(_calls().gdr_norm_fwd,
+         _NORM.pack(x2.data_ptr(), res, weight.data_ptr(), m, d, x2.stride(0), row, eps, code, out.data_ptr() if res else 0, *to),
+         dev)
     return y, scales, out
 
 
@@ -441,22 +471,23 @@ class _ResidualRmsNorm(torch.autograd.Function):
         return y, out if ctx.added else x.view_as(x)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dy, dsum):
+        _once()
         r, weight = ctx.saved_tensors
-        d = r.shape[-1]
+        shape, where = r.shape, r.device
+        d = shape[-1]
         m = r.numel() // d
-        dy = torch.zeros(r.shape, dtype=r.dtype, device=r.device) if dy is None else _grad(dy, r)
+        dy = torch.zeros(shape, dtype=r.dtype, device=where) if dy is None else _grad(dy, r)
         dsum = _grad(dsum, r)
         r = r.contiguous()
-        dr = torch.empty(r.shape, dtype=r.dtype, device=r.device)
-        dweight = torch.empty_like(weight)
+        dr = _empty(shape, dtype=r.dtype, device=where)
+        dweight = _empty((d,), dtype=_F32, device=where)
         lib = _calls()
         size = lib.gdr_norm_bwd_workspace_size(m, d)
-        ws = torch.empty(size, dtype=torch.uint8, device=r.device)
-        a = _NormBwdArgs(r.data_ptr(), dy.data_ptr(), _ptr(dsum), weight.data_ptr(), m, d, ctx.eps, _DTYPES[r.dtype],
-                         dr.data_ptr(), dweight.data_ptr(), ws.data_ptr(), size)
-        _run(lib.gdr_norm_bwd, a, r.device)
+        ws = _empty(size, dtype=torch.uint8, device=where)
+        _run(lib.gdr_norm_bwd,
+             _NORM_BWD.pack(r.data_ptr(), dy.data_ptr(), _ptr(dsum), weight.data_ptr(), m, d, ctx.eps, _DTYPES[r.dtype],
+                            dr.data_ptr(), dweight.data_ptr(), ws.data_ptr(), size), r.get_device())
         return dr, dweight, dr if ctx.added else None, None
 
 
@@ -488,23 +519,23 @@ def block_matmul_fp8(a, a_scales, b, b_scales, out_dtype=torch.bfloat16):
 
     a [M, K] and b [N, K] float8_e4m3fn, K a multiple of 16; a_scales [ceil(K / 128), M] and b_scales
     [ceil(N / 128), ceil(K / 128)] fp32; out_dtype bf16 or fp32.  Returns out [M, N].  No gradient."""
-    f8 = torch.float8_e4m3fn
-    if not a.is_cuda:
+    f8, dev = torch.float8_e4m3fn, a.get_device()
+    if dev < 0:
         _fail(1, "a must live on the GPU")
     if a.dim() != 2 or b.dim() != 2:
         _fail(2, f"a must be [M, K] and b [N, K] (got {tuple(a.shape)}, {tuple(b.shape)})")
     (m, k), n = a.shape, b.shape[0]
-    _param("a", a, a, (m, k), f8)
-    _param("b", b, a, (n, k), f8)
     blocks = -(-k // 128)
-    _param("a_scales", a_scales, a, (blocks, m))
-    _param("b_scales", b_scales, a, (-(-n // 128), blocks))
+    _param("a", a, dev, (m, k), f8)
+    _param("b", b, dev, (n, k), f8)
+    _param("a_scales", a_scales, dev, (blocks, m))
+    _param("b_scales", b_scales, dev, (-(-n // 128), blocks))
     code = _DTYPES.get(out_dtype)
     if code is None:
         _fail(3, f"out_dtype must be torch.bfloat16 or torch.float32 (got {out_dtype})")
     if _wants_grad(a_scales, b_scales):
         _fail(1, "block_matmul_fp8 has no gradient: call it under torch.no_grad()")
-    out = torch.empty((m, n), dtype=out_dtype, device=a.device)
-    args = _Fp8Args(a.data_ptr(), b.data_ptr(), a_scales.data_ptr(), b_scales.data_ptr(), m, n, k, code, out.data_ptr())
-    _run(_calls().gdr_fp8_matmul, args, a.device)
+    out = _empty((m, n), dtype=out_dtype, device=a.device)
+    _run(_calls().gdr_fp8_matmul,
+         _FP8.pack(a.data_ptr(), b.data_ptr(), a_scales.data_ptr(), b_scales.data_ptr(), m, n, k, code, out.data_ptr()), dev)
     return out
