@@ -33,7 +33,7 @@ __device__ unsigned g_ssm_status;
 constexpr int kThreads = 128;          // scanning threads; as many help
 constexpr int kTile = 32;              // tokens staged at a time (forward)
 constexpr int kBack = GDR_SSM_STRIDE;  // tokens of a backward tile, and between checkpoints
-constexpr int kGroup = 4;              // tokens of a backward tile whose latencies overlap
+constexpr int kGroup = 8;              // tokens of a backward tile whose latencies overlap
 
 struct SsmP {
     const void *x, *dt, *z, *Bm, *Cm, *dy;
@@ -442,7 +442,7 @@ __device__ __forceinline__ void put_fold(float *to, float2 v) {
 }
 
 template <typename T, int kL, bool kVec, bool kSum>
-__global__ void __launch_bounds__(2 * kThreads, 1) k_ssm_bwd(const SsmP p) {
+__global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_bwd(const SsmP p) {
     using W = Place<kL>;
     using S = BwdSmem<kL, kSum>;
     constexpr int kCh = W::kCh, kN = W::kN;
