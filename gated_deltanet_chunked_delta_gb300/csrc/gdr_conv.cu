@@ -6,18 +6,26 @@
 //   dw_j = sum_t dp_t x_{t-W+1+j};  dbias = sum_t dp_t
 //
 // Bound by memory: the forward reads x and writes y once, the backward reads x
-// and dy and writes dx.  A thread owns eight neighbouring channels (16-byte
-// accesses in bf16) and walks a run of tokens with the last W - 1 inputs in
-// registers, so an input is read from memory once per run plus the W - 1
-// tokens of overlap between runs, which neighbouring threads' lines cover.
+// and dy and writes dx.  A thread owns kE neighbouring channels and walks a run
+// of tokens with the last W - 1 inputs in registers, so an input is read from
+// memory once per run plus the W - 1 tokens of overlap between runs, which
+// neighbouring threads' lines cover.  kE is 4 where rows allow it, else 2 or 1:
+// neighbouring lanes always read neighbouring channels.  (Eight channels a
+// thread cost the occupancy that hides the reads; as eight scalar reads a
+// thread, for odd widths, they took 2.3 times as long.)
+#include <cstring>
+#include <initializer_list>
+
 #include "gdr_layer.h"
 
 namespace {
 
 __device__ unsigned g_conv_status;
 
-constexpr int kCols = 32;   // 8-channel columns of a CTA (one warp)
-constexpr int kRuns = 8;    // token runs of a CTA (its warps)
+constexpr int kCols = 32;   // columns of kE channels of a CTA (one warp)
+constexpr int kRuns = 8;    // token runs of a CTA (its warps), forward
+constexpr int kRunsB = 4;   // and backward
+constexpr int kAheadF = 8, kAheadB = 4;  // tokens read at a time (backward of 8192 x 4096: 99 us with 4, 121 with 8)
 
 struct ConvP {
     const void *x, *h0, *dy, *dht;
@@ -29,87 +37,151 @@ struct ConvP {
     int T, D, silu, run;  // run: tokens of a thread
 };
 
+// kE neighbouring elements as they lie in memory, none where a thread has no channel.
+template <typename T, int kE>
+struct Raw;
+template <>
+struct Raw<bf16_t, 4> {
+    uint2 r;
+};
+template <>
+struct Raw<float, 4> {
+    uint4 r;
+};
+template <>
+struct Raw<bf16_t, 2> {
+    uint32_t r;
+};
+template <>
+struct Raw<float, 2> {
+    uint2 r;
+};
+template <typename T>
+struct Raw<T, 1> {
+    T r;
+};
+template <typename T, int kE>
+__device__ __forceinline__ Raw<T, kE> load_e(const T *p, bool on) {
+    Raw<T, kE> v;
+    memset(&v, 0, sizeof(v));
+    if (on) v = *reinterpret_cast<const Raw<T, kE> *>(p);
+    return v;
+}
+template <typename T, int kE>
+__device__ __forceinline__ void unpack_e(const Raw<T, kE> &v, float (&f)[kE]) {
+    if constexpr (kE == 1) {
+        f[0] = to_f(v.r);
+    } else {
+        uint32_t w[sizeof(v) / 4];
+        memcpy(w, &v, sizeof(v));
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(v) / 4); ++i) {
+            if constexpr (sizeof(T) == 2) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                f[i] = __uint_as_float(w[i]);
+            }
+        }
+    }
+}
+template <typename T, int kE>
+__device__ __forceinline__ void store_e(T *p, const float (&f)[kE], bool on) {
+    if (!on) return;
+    if constexpr (kE == 1) {
+        from_f(p[0], f[0]);
+    } else {
+        Raw<T, kE> v;
+        uint32_t w[sizeof(v) / 4];
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(v) / 4); ++i) {
+            if constexpr (sizeof(T) == 2) w[i] = pack2(f[2 * i], f[2 * i + 1]);
+            else w[i] = __float_as_uint(f[i]);
+        }
+        memcpy(&v, w, sizeof(v));
+        *reinterpret_cast<Raw<T, kE> *>(p) = v;
+    }
+}
+
 // Inputs of a sequence before its first token: row i of its initial state.
-template <typename T, int W, bool kVec>
-__device__ __forceinline__ void init_row(const ConvP &p, int seq, int i, int ch, int nv, float (&f)[8]) {
+template <typename T, int W, int kE>
+__device__ __forceinline__ void init_row(const ConvP &p, int seq, int i, int ch, bool on, float (&f)[kE]) {
     if (!p.h0 || i < 0 || i >= W - 1) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 0.f;
+        for (int e = 0; e < kE; ++e) f[e] = 0.f;
         return;
     }
-    unpack8(load8<T, kVec>(static_cast<const T *>(p.h0) + ((long long)seq * (W - 1) + i) * p.D + ch, nv), f);
+    unpack_e<T, kE>(load_e<T, kE>(static_cast<const T *>(p.h0) + ((long long)seq * (W - 1) + i) * p.D + ch, on), f);
 }
 
 // The input of token t (of the sequence starting at s0), t - s0 may be negative.
-template <typename T, int W, bool kVec>
-__device__ __forceinline__ void input_at(const ConvP &p, const T *x, int seq, int s0, int t, int ch, int nv, float (&f)[8]) {
-    if (t >= s0 && t >= 0) unpack8(load8<T, kVec>(x + (long long)t * p.x_row + ch, nv), f);
-    else init_row<T, W, kVec>(p, seq, t - s0 + W - 1, ch, nv, f);
+template <typename T, int W, int kE>
+__device__ __forceinline__ void input_at(const ConvP &p, const T *x, int seq, int s0, int t, int ch, bool on, float (&f)[kE]) {
+    if (t >= s0 && t >= 0) unpack_e<T, kE>(load_e<T, kE>(x + (long long)t * p.x_row + ch, on), f);
+    else init_row<T, W, kE>(p, seq, t - s0 + W - 1, ch, on, f);
 }
 
 // The state that a sequence without tokens hands on is the one it got.
-template <typename T, int W, bool kVec>
-__device__ __forceinline__ void pass_on(const ConvP &p, int seq, int ch, int nv) {
+template <typename T, int W, int kE>
+__device__ __forceinline__ void pass_on(const ConvP &p, int seq, int ch, bool on) {
     if (!p.ht) return;
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
-        float f[8];
-        init_row<T, W, kVec>(p, seq, i, ch, nv, f);
-        store8<T, kVec>(static_cast<T *>(p.ht) + ((long long)seq * (W - 1) + i) * p.D + ch, f, nv);
+        float f[kE];
+        init_row<T, W, kE>(p, seq, i, ch, on, f);
+        store_e<T, kE>(static_cast<T *>(p.ht) + ((long long)seq * (W - 1) + i) * p.D + ch, f, on);
     }
 }
 
-template <int W, bool kVec>
-__device__ __forceinline__ void load_weights(const float *weight, const float *bias, int ch, int nv, float (&w)[W][8],
-                                             float (&b)[8]) {
-    if constexpr (kVec) {  // eight channels' taps are one aligned run of 32 W bytes
-        float f[8 * W];
+template <int W, int kE>
+__device__ __forceinline__ void load_weights(const float *weight, const float *bias, int ch, bool on, float (&w)[W][kE],
+                                             float (&b)[kE]) {
+    if constexpr (kE >= 4) {  // the channels' taps are one aligned run of 4 kE W bytes
+        float f[kE * W];
 #pragma unroll
-        for (int i = 0; i < 2 * W; ++i)
-            *reinterpret_cast<float4 *>(f + 4 * i) = reinterpret_cast<const float4 *>(weight + (long long)ch * W)[i];
+        for (int i = 0; i < kE * W / 4; ++i)
+            *reinterpret_cast<float4 *>(f + 4 * i) = on ? reinterpret_cast<const float4 *>(weight + (long long)ch * W)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            b[e] = bias ? bias[ch + e] : 0.f;
+        for (int e = 0; e < kE; ++e)
 #pragma unroll
             for (int j = 0; j < W; ++j) w[j][e] = f[e * W + j];
-        }
     } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        b[e] = e < nv && bias ? bias[ch + e] : 0.f;
+        for (int e = 0; e < kE; ++e)
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][e] = e < nv ? weight[(long long)(ch + e) * W + j] : 0.f;
+            for (int j = 0; j < W; ++j) w[j][e] = on ? weight[(long long)(ch + e) * W + j] : 0.f;
     }
-    }
+#pragma unroll
+    for (int e = 0; e < kE; ++e) b[e] = on && bias ? bias[ch + e] : 0.f;
 }
 
-template <typename T, int W, bool kVec>
+template <typename T, int W, int kE>
 __global__ void __launch_bounds__(kCols *kRuns) k_conv_fwd(const ConvP p) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_bounds(p.seqs, &g_conv_status);
-    const int ch = (blockIdx.x * kCols + threadIdx.x % kCols) * 8, nv = min(8, p.D - ch);
-    if (nv <= 0) return;
+    const int ch = (blockIdx.x * kCols + threadIdx.x % kCols) * kE;
+    const bool on = ch < p.D;
+    if (!on) return;
     const int bz = blockIdx.z;
     const T *x = static_cast<const T *>(p.x) + bz * p.x_batch;
     T *y = static_cast<T *>(p.y) + (long long)bz * p.T * p.D;
     const int t0 = (blockIdx.y * kRuns + threadIdx.x / kCols) * p.run, t1 = min(t0 + p.run, p.T);
     const int sbase = p.seqs.cu ? 0 : bz;  // index of this row's first sequence
     if (t0 == 0 && p.seqs.cu)              // leading sequences without tokens
-        for (int n = 0; n < p.seqs.n && p.seqs.bound(n + 1) <= 0; ++n) pass_on<T, W, kVec>(p, n, ch, nv);
+        for (int n = 0; n < p.seqs.n && p.seqs.bound(n + 1) <= 0; ++n) pass_on<T, W, kE>(p, n, ch, on);
     if (t0 >= t1) return;
-    float w[W][8], b[8];
-    load_weights<W, kVec>(p.weight, p.bias, ch, nv, w, b);
+    float w[W][kE], b[kE];
+    load_weights<W, kE>(p.weight, p.bias, ch, on, w, b);
     int n = p.seqs.find(t0), s0 = p.seqs.bound(n), s1 = p.seqs.bound(n + 1);
-    float hist[W - 1][8];  // inputs of t - W + 1 .. t - 1
+    float hist[W - 1][kE];  // inputs of t - W + 1 .. t - 1
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) input_at<T, W, kVec>(p, x, sbase + n, s0, t0 - (W - 1) + j, ch, nv, hist[j]);
-    constexpr int kAhead = 4;
-    for (int tb = t0; tb < t1; tb += kAhead) {
-        Raw8<T> raw[kAhead];
+    for (int j = 0; j < W - 1; ++j) input_at<T, W, kE>(p, x, sbase + n, s0, t0 - (W - 1) + j, ch, on, hist[j]);
+    for (int tb = t0; tb < t1; tb += kAheadF) {
+        Raw<T, kE> raw[kAheadF];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            raw[i] = load8<T, kVec>(x + (long long)min(tb + i, p.T - 1) * p.x_row + ch, tb + i < t1 ? nv : 0);
+        for (int i = 0; i < kAheadF; ++i)
+            raw[i] = load_e<T, kE>(x + (long long)min(tb + i, p.T - 1) * p.x_row + ch, tb + i < t1);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < kAheadF; ++i) {
             const int t = tb + i;
             if (t >= t1) break;
             if (t >= s1 && n + 1 < p.seqs.count()) {  // the next sequence with tokens
@@ -119,12 +191,12 @@ __global__ void __launch_bounds__(kCols *kRuns) k_conv_fwd(const ConvP p) {
                     s1 = p.seqs.bound(n + 1);
                 } while (s1 <= t && n + 1 < p.seqs.count());
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) init_row<T, W, kVec>(p, sbase + n, j, ch, nv, hist[j]);
+                for (int j = 0; j < W - 1; ++j) init_row<T, W, kE>(p, sbase + n, j, ch, on, hist[j]);
             }
-            float cur[8], o[8];
-            unpack8(raw[i], cur);
+            float cur[kE], o[kE];
+            unpack_e<T, kE>(raw[i], cur);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kE; ++e) {
                 float a = fmaf(w[W - 1][e], cur[e], b[e]);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][e], hist[j][e], a);
@@ -133,119 +205,126 @@ __global__ void __launch_bounds__(kCols *kRuns) k_conv_fwd(const ConvP p) {
                 for (int j = 0; j + 1 < W - 1; ++j) hist[j][e] = hist[j + 1][e];
                 hist[W - 2][e] = cur[e];
             }
-            store8<T, kVec>(y + (long long)t * p.D + ch, o, nv);
+            store_e<T, kE>(y + (long long)t * p.D + ch, o, on);
             if (p.ht && t == s1 - 1) {
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
-                    store8<T, kVec>(static_cast<T *>(p.ht) + ((long long)(sbase + n) * (W - 1) + j) * p.D + ch, hist[j], nv);
+                    store_e<T, kE>(static_cast<T *>(p.ht) + ((long long)(sbase + n) * (W - 1) + j) * p.D + ch, hist[j], on);
                 // the sequences without tokens that follow
                 if (p.seqs.cu)
-                    for (int m = n + 1; m < p.seqs.n && p.seqs.bound(m + 1) <= s1; ++m) pass_on<T, W, kVec>(p, m, ch, nv);
+                    for (int m = n + 1; m < p.seqs.n && p.seqs.bound(m + 1) <= s1; ++m) pass_on<T, W, kE>(p, m, ch, on);
             }
         }
     }
 }
 
-// Walks the tokens of a run and the W - 1 after it: token t's dp belongs to
-// the weights' gradient if t is in the run, and the W-th last token's dx is
-// then complete.  The CTA's runs are added through shared memory in order.
-template <typename T, int W, bool kVec>
-__global__ void __launch_bounds__(kCols *kRuns) k_conv_bwd(const ConvP p) {
-    __shared__ float red[kRuns][kCols][8];
+// Walks the tokens of a run and the W - 1 after it.  Token t's dp belongs to
+// the weights' gradient if t is in the run; it is added to the gradients of the
+// W - 1 tokens before it (as far as they are of its sequence), which wait in
+// registers, and completes that of token t - W + 1.  The CTA's runs are added
+// through shared memory in order.
+template <typename T, int W, int kE>
+__global__ void __launch_bounds__(kCols *kRunsB) k_conv_bwd(const ConvP p) {
+    __shared__ float red[kRunsB][kCols][kE];
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_bounds(p.seqs, &g_conv_status);
     const int col = threadIdx.x % kCols, rn = threadIdx.x / kCols;
-    const int ch = (blockIdx.x * kCols + col) * 8, nv = min(8, p.D - ch);
+    const int ch = (blockIdx.x * kCols + col) * kE;
+    const bool on = ch < p.D;
     const int bz = blockIdx.z;
     const T *x = static_cast<const T *>(p.x) + bz * p.x_batch;
     const T *dy = static_cast<const T *>(p.dy) + (long long)bz * p.T * p.D;
     T *dx = static_cast<T *>(p.dx) + (long long)bz * p.T * p.D;
-    const int t0 = (blockIdx.y * kRuns + rn) * p.run, t1 = min(t0 + p.run, p.T);
+    const int t0 = (blockIdx.y * kRunsB + rn) * p.run, t1 = min(t0 + p.run, p.T);
     const int sbase = p.seqs.cu ? 0 : bz;
-    float dw[W + 1][8];  // taps, bias
+    float dw[W + 1][kE];  // taps, bias
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[j][e] = 0.f;
-    if (nv > 0 && t0 < t1) {
-        float w[W][8], b[8], hist[W - 1][8], dps[W][8];  // dps[i]: dp of token t - W + 1 + i
-        int seq_of[W], end_of[W];
-        load_weights<W, kVec>(p.weight, p.bias, ch, nv, w, b);
+        for (int e = 0; e < kE; ++e) dw[j][e] = 0.f;
+    if (on && t0 < t1) {
+        float w[W][kE], b[kE], hist[W - 1][kE], wait[W - 1][kE];  // wait[i]: gradient of token t - W + 1 + i
+        load_weights<W, kE>(p.weight, p.bias, ch, on, w, b);
         int n = p.seqs.find(t0), s0 = p.seqs.bound(n), s1 = p.seqs.bound(n + 1);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) input_at<T, W, kVec>(p, x, sbase + n, s0, t0 - (W - 1) + j, ch, nv, hist[j]);
+        for (int j = 0; j < W - 1; ++j) {
+            input_at<T, W, kE>(p, x, sbase + n, s0, t0 - (W - 1) + j, ch, on, hist[j]);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            seq_of[j] = end_of[j] = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dps[j][e] = 0.f;
+            for (int e = 0; e < kE; ++e) wait[j][e] = 0.f;
         }
-        for (int t = t0; t < t1 + W - 1; ++t) {
+        for (int tb = t0; tb < t1 + W - 1; tb += kAheadB) {
+            Raw<T, kE> rx[kAheadB], rg[kAheadB];
 #pragma unroll
-            for (int j = 0; j + 1 < W; ++j) {
-                seq_of[j] = seq_of[j + 1];
-                end_of[j] = end_of[j + 1];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) dps[j][e] = dps[j + 1][e];
+            for (int i = 0; i < kAheadB; ++i) {
+                const int t = min(tb + i, p.T - 1);
+                const bool nl = tb + i < min(t1 + W - 1, p.T);
+                rx[i] = load_e<T, kE>(x + (long long)t * p.x_row + ch, nl);
+                rg[i] = load_e<T, kE>(dy + (long long)t * p.D + ch, nl);
             }
-            if (t < p.T) {
-                float cur[8], g[8];
-                unpack8(load8<T, kVec>(x + (long long)t * p.x_row + ch, nv), cur);
-                unpack8(load8<T, kVec>(dy + (long long)t * p.D + ch, nv), g);
-                if (t >= s1 && n + 1 < p.seqs.count()) {
-                    do {
-                        ++n;
-                        s0 = s1;
-                        s1 = p.seqs.bound(n + 1);
-                    } while (s1 <= t && n + 1 < p.seqs.count());
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) init_row<T, W, kVec>(p, sbase + n, j, ch, nv, hist[j]);
-                }
-                seq_of[W - 1] = sbase + n;
-                end_of[W - 1] = s1;
-                const bool mine = t < t1;
+            for (int i = 0; i < kAheadB; ++i) {
+                const int t = tb + i;
+                if (t >= t1 + W - 1) break;
+                float dp[kE];
+                if (t < p.T) {
+                    if (t >= s1 && n + 1 < p.seqs.count()) {
+                        do {
+                            ++n;
+                            s0 = s1;
+                            s1 = p.seqs.bound(n + 1);
+                        } while (s1 <= t && n + 1 < p.seqs.count());
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float a = fmaf(w[W - 1][e], cur[e], b[e]);
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][e], hist[j][e], a);
-                    float d = g[e];
-                    if (p.silu) {
-                        const float s = sigmoidf(a);
-                        d *= s * fmaf(a, 1.f - s, 1.f);
+                        for (int j = 0; j < W - 1; ++j) init_row<T, W, kE>(p, sbase + n, j, ch, on, hist[j]);
                     }
-                    dps[W - 1][e] = d;
-                    if (mine) {
+                    float cur[kE], g[kE];
+                    unpack_e<T, kE>(rx[i], cur);
+                    unpack_e<T, kE>(rg[i], g);
+                    const bool mine = t < t1;
 #pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(d, hist[j][e], dw[j][e]);
-                        dw[W - 1][e] = fmaf(d, cur[e], dw[W - 1][e]);
-                        dw[W][e] += d;
+                    for (int e = 0; e < kE; ++e) {
+                        float a = fmaf(w[W - 1][e], cur[e], b[e]);
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][e], hist[j][e], a);
+                        float d = g[e];
+                        if (p.silu) {
+                            const float s = sigmoidf(a);
+                            d *= s * fmaf(a, 1.f - s, 1.f);
+                        }
+                        dp[e] = d;
+                        if (mine) {
+#pragma unroll
+                            for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(d, hist[j][e], dw[j][e]);
+                            dw[W - 1][e] = fmaf(d, cur[e], dw[W - 1][e]);
+                            dw[W][e] += d;
+                        }
+#pragma unroll
+                        for (int j = 0; j + 1 < W - 1; ++j) hist[j][e] = hist[j + 1][e];
+                        hist[W - 2][e] = cur[e];
                     }
+                } else {
 #pragma unroll
-                    for (int j = 0; j + 1 < W - 1; ++j) hist[j][e] = hist[j + 1][e];
-                    hist[W - 2][e] = cur[e];
+                    for (int e = 0; e < kE; ++e) dp[e] = 0.f;
                 }
-            } else {
+                const int old = t < p.T ? t - s0 : W;  // tokens of this one's sequence before it
+                float o[kE];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dps[W - 1][e] = 0.f;
-            }
-            const int s = t - (W - 1);
-            if (s >= t0 && s < t1) {
-                float o[8];
+                for (int j = 0; j < W; ++j) {  // to the token W - 1 - j before this one
+                    const bool same = W - 1 - j <= old;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = 0.f;
-#pragma unroll
-                for (int i = 0; i < W; ++i)  // dp of token s + i times tap W - 1 - i
-                    if (s + i < end_of[0])
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = fmaf(w[W - 1 - i][e], dps[i][e], o[e]);
-                const int k = W - 1 - (end_of[0] - s);  // row of the final state that holds token s
-                if (p.dht && k >= 0 && k < W - 1) {
-                    float f[8];
-                    unpack8(load8<T, kVec>(static_cast<const T *>(p.dht) + ((long long)seq_of[0] * (W - 1) + k) * p.D + ch, nv), f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] += f[e];
+                    for (int e = 0; e < kE; ++e) {
+                        const float v = fmaf(same ? w[j][e] : 0.f, dp[e], j < W - 1 ? wait[j < W - 1 ? j : 0][e] : 0.f);
+                        if (j == 0) o[e] = v;
+                        else wait[j - 1 < 0 ? 0 : j - 1][e] = v;
+                    }
                 }
-                store8<T, kVec>(dx + (long long)s * p.D + ch, o, nv);
+                const int k = W - 1 - (s1 - t);  // row of the final state that holds token t
+                if (p.dht && t < p.T && k >= 0 && k < W - 1) {
+                    float f[kE];
+                    unpack_e<T, kE>(load_e<T, kE>(static_cast<const T *>(p.dht) + ((long long)(sbase + n) * (W - 1) + k) * p.D + ch, on), f);
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) wait[W - 2][e] += f[e];
+                }
+                const int s = t - (W - 1);
+                if (s >= t0 && s < t1) store_e<T, kE>(dx + (long long)s * p.D + ch, o, on);
             }
         }
     }
@@ -254,14 +333,14 @@ __global__ void __launch_bounds__(kCols *kRuns) k_conv_bwd(const ConvP p) {
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) red[rn][col][e] = dw[j][e];
+        for (int e = 0; e < kE; ++e) red[rn][col][e] = dw[j][e];
         __syncthreads();
-        const int c = threadIdx.x >> 3, e = threadIdx.x & 7;  // 256 threads, 256 channels
-        const int d = (blockIdx.x * kCols + c) * 8 + e;
-        if (d < p.D) {
+        for (int i = threadIdx.x; i < kCols * kE; i += kCols * kRunsB) {
+            const int d = blockIdx.x * kCols * kE + i;
+            if (d >= p.D) break;
             float a = 0.f;
 #pragma unroll
-            for (int r = 0; r < kRuns; ++r) a += red[r][c][e];
+            for (int r = 0; r < kRunsB; ++r) a += red[r][i / kE][i % kE];
             part[(long long)j * p.D + d] = a;
         }
     }
@@ -331,39 +410,40 @@ struct StepP {
     int rows, D, silu;
 };
 
-template <typename T, int W, bool kVec>
+template <typename T, int W, int kE>
 __global__ void k_conv_step(const StepP p) {
-    const int ch = (blockIdx.x * blockDim.x + threadIdx.x) * 8, nv = min(8, p.D - ch), r = blockIdx.y;
-    if (nv <= 0) return;
+    const int ch = (blockIdx.x * blockDim.x + threadIdx.x) * kE, r = blockIdx.y;
+    const bool on = ch < p.D;
+    if (!on) return;
     const long long slot = p.slots ? p.slots[r] : r;
     T *y = static_cast<T *>(p.y) + (long long)r * p.D + ch;
-    float o[8];
+    float o[kE];
     if (slot < 0 || slot >= p.n_slots) {
         if (slot >= 0 && threadIdx.x == 0) atomicOr(&g_conv_status, kStatusIndex);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 0.f;
-        store8<T, kVec>(y, o, nv);
+        for (int e = 0; e < kE; ++e) o[e] = 0.f;
+        store_e<T, kE>(y, o, on);
         return;
     }
     T *st = static_cast<T *>(p.state) + slot * (W - 1) * p.D + ch;
-    Raw8<T> raw[W];
+    Raw<T, kE> raw[W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) raw[j] = load8<T, kVec>(st + (long long)j * p.D, nv);
-    raw[W - 1] = load8<T, kVec>(static_cast<const T *>(p.x) + r * p.x_row + ch, nv);
-    float w[W][8];
-    load_weights<W, kVec>(p.weight, p.bias, ch, nv, w, o);
+    for (int j = 0; j < W - 1; ++j) raw[j] = load_e<T, kE>(st + (long long)j * p.D, on);
+    raw[W - 1] = load_e<T, kE>(static_cast<const T *>(p.x) + r * p.x_row + ch, on);
+    float w[W][kE];
+    load_weights<W, kE>(p.weight, p.bias, ch, on, w, o);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        float f[8];
-        unpack8(raw[j], f);
+        float f[kE];
+        unpack_e<T, kE>(raw[j], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = fmaf(w[j][e], f[e], o[e]);
-        if (j > 0) store8<T, kVec>(st + (long long)(j - 1) * p.D, f, nv);
+        for (int e = 0; e < kE; ++e) o[e] = fmaf(w[j][e], f[e], o[e]);
+        if (j > 0) store_e<T, kE>(st + (long long)(j - 1) * p.D, f, on);
     }
     if (p.silu)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= sigmoidf(o[e]);
-    store8<T, kVec>(y, o, nv);
+        for (int e = 0; e < kE; ++e) o[e] *= sigmoidf(o[e]);
+    store_e<T, kE>(y, o, on);
 }
 
 // ---- host ------------------------------------------------------------------
@@ -386,18 +466,29 @@ int conv_seqs(const gdr_conv_args *a, Seqs *s) {
     return GDR_OK;
 }
 
-// Tokens of a thread: long runs read less twice, short ones fill the SMs.
-int run_length(long long B, long long T, long long D, bool bwd) {
-    const long long cols = (D + 8 * kCols - 1) / (8 * kCols);
-    int run = bwd ? 64 : 16;
-    while (run > 4 && cols * B * ((T + (long long)run * kRuns - 1) / ((long long)run * kRuns)) < 2LL * layer_sms()) run /= 2;
-    while ((T + (long long)run * kRuns - 1) / ((long long)run * kRuns) > 65535) run *= 2;
-    return run;
+// Channels of a thread: as many as rows and pointers allow to be moved at once.
+int channels(long long D, std::initializer_list<long long> strides, int dtype, const float *weight,
+             std::initializer_list<const void *> ptrs) {
+    const int size = dtype == GDR_BF16 ? 2 : 4;
+    auto ok = [&](int e) {
+        if (D % e) return false;
+        for (long long v : strides)
+            if (v % e) return false;
+        for (const void *p : ptrs)
+            if (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(e * size - 1)) return false;
+        return true;
+    };
+    return ok(4) && multiple16(weight) ? 4 : ok(2) ? 2 : 1;
 }
 
-bool vec_ok(long long D, long long row, long long batch, int dtype) {
-    const long long q = dtype == GDR_BF16 ? 8 : 4;
-    return D % 8 == 0 && row % q == 0 && batch % q == 0;
+// Tokens of a thread: long runs read less twice, short ones fill the SMs.
+int run_length(long long B, long long T, long long D, int e, bool bwd) {
+    const long long cols = (D + e * kCols - 1) / (e * kCols), runs = bwd ? kRunsB : kRuns;
+    int run = bwd ? 64 : 32;
+    auto blocks = [&] { return (T + run * runs - 1) / (run * runs); };
+    while (run > 4 && cols * B * blocks() < 3LL * layer_sms()) run /= 2;
+    while (blocks() > 65535) run *= 2;
+    return run;
 }
 
 void fill(const gdr_conv_args *a, const Seqs &s, ConvP *p) {
@@ -407,10 +498,12 @@ void fill(const gdr_conv_args *a, const Seqs &s, ConvP *p) {
 }
 
 template <typename F>
-void by_type(int dtype, int W, bool vec, F f) {
+void by_type(int dtype, int W, int e, F f) {
     auto w = [&](auto t) {
         auto v = [&](auto c) {
-            if (vec) f(t, c, std::true_type{}); else f(t, c, std::false_type{});
+            if (e == 4) f(t, c, std::integral_constant<int, 4>{});
+            else if (e == 2) f(t, c, std::integral_constant<int, 2>{});
+            else f(t, c, std::integral_constant<int, 1>{});
         };
         if (W == 2) v(std::integral_constant<int, 2>{});
         else if (W == 3) v(std::integral_constant<int, 3>{});
@@ -419,8 +512,8 @@ void by_type(int dtype, int W, bool vec, F f) {
     if (dtype == GDR_BF16) w(bf16_t{}); else w(float{});
 }
 
-long long bwd_blocks(long long B, long long T, long long D) {
-    const long long span = (long long)run_length(B, T, D, true) * kRuns;
+long long bwd_blocks(long long B, long long T, long long D, int e) {
+    const long long span = (long long)run_length(B, T, D, e, true) * kRunsB;
     return B * ((T + span - 1) / span);
 }
 
@@ -461,11 +554,10 @@ int gdr_conv_fwd(const gdr_conv_args *a, void *stream) {
                                       : cudaMemsetAsync(a->ht, 0, bytes, static_cast<cudaStream_t>(stream));
         return err == cudaSuccess ? GDR_OK : layer_fail(GDR_ERR_CUDA, "conv: %s", cudaGetErrorString(err));
     }
-    p.run = run_length(a->B, a->T, a->D, false);
-    const bool vec = vec_ok(a->D, a->x_row, a->x_batch, a->dtype) && multiple16(a->x) && multiple16(a->weight) && multiple16(a->y) &&
-                     multiple16(a->h0) && multiple16(a->ht);
+    const int vec = channels(a->D, {a->x_row, a->x_batch}, a->dtype, a->weight, {a->x, a->y, a->h0, a->ht});
+    p.run = run_length(a->B, a->T, a->D, vec, false);
     const long long span = (long long)p.run * kRuns;
-    const dim3 grid((unsigned)((a->D + 8 * kCols - 1) / (8 * kCols)), (unsigned)(any ? (a->T + span - 1) / span : 1), (unsigned)a->B);
+    const dim3 grid((unsigned)((a->D + vec * kCols - 1) / (vec * kCols)), (unsigned)(any ? (a->T + span - 1) / span : 1), (unsigned)a->B);
     by_type(a->dtype, a->W, vec, [&](auto t, auto w, auto v) {
         k_conv_fwd<decltype(t), decltype(w)::value, decltype(v)::value><<<grid, kCols * kRuns, 0, static_cast<cudaStream_t>(stream)>>>(p);
     });
@@ -474,7 +566,9 @@ int gdr_conv_fwd(const gdr_conv_args *a, void *stream) {
 
 size_t gdr_conv_bwd_workspace_size(long long B, long long T, long long D, int W) {
     if (conv_sizes(B, T, D, W, GDR_BF16)) return 0;
-    return (size_t)(bwd_blocks(B, T, D) * (W + 1) * D * 4 + 16);
+    long long blocks = 0;  // whichever way the call's rows can be read
+    for (int e : {4, 2, 1}) blocks = std::max(blocks, bwd_blocks(B, T, D, e));
+    return (size_t)(blocks * (W + 1) * D * 4 + 16);
 }
 
 int gdr_conv_bwd(const gdr_conv_args *a, void *stream) {
@@ -499,17 +593,16 @@ int gdr_conv_bwd(const gdr_conv_args *a, void *stream) {
     fill(a, s, &p);
     p.dy = a->dy; p.dht = a->dht; p.dx = a->dx; p.dh0 = a->dh0;
     p.part = static_cast<float *>(a->workspace);
-    p.run = run_length(a->B, a->T, a->D, true);
-    const bool vec = vec_ok(a->D, a->x_row, a->x_batch, a->dtype) && multiple16(a->x) && multiple16(a->weight) && multiple16(a->dy) &&
-                     multiple16(a->dx) && multiple16(a->h0) && multiple16(a->dht);
-    const long long span = (long long)p.run * kRuns;
-    const dim3 grid((unsigned)((a->D + 8 * kCols - 1) / (8 * kCols)), (unsigned)((a->T + span - 1) / span), (unsigned)a->B);
-    const long long blocks = bwd_blocks(a->B, a->T, a->D);
+    const int vec = channels(a->D, {a->x_row, a->x_batch}, a->dtype, a->weight, {a->x, a->dy, a->dx, a->h0, a->dht});
+    p.run = run_length(a->B, a->T, a->D, vec, true);
+    const long long span = (long long)p.run * kRunsB;
+    const dim3 grid((unsigned)((a->D + vec * kCols - 1) / (vec * kCols)), (unsigned)((a->T + span - 1) / span), (unsigned)a->B);
+    const long long blocks = bwd_blocks(a->B, a->T, a->D, vec);
     if (a->dh0 && (a->n_seqs > 65535)) return layer_fail(GDR_ERR_SHAPE, "conv backward: dh0 of more than 65535 sequences");
     by_type(a->dtype, a->W, vec, [&](auto t, auto w, auto v) {
         using E = decltype(t);
         constexpr int W = decltype(w)::value;
-        if (any) k_conv_bwd<E, W, decltype(v)::value><<<grid, kCols * kRuns, 0, st>>>(p);
+        if (any) k_conv_bwd<E, W, decltype(v)::value><<<grid, kCols * kRunsB, 0, st>>>(p);
         k_conv_bwd_sum<W><<<dim3((unsigned)((a->D + 255) / 256), W + 1), 256, 0, st>>>(p.part, (int)blocks, (int)a->D, a->dweight, a->dbias);
         if (a->dh0) k_conv_bwd_init<E, W><<<dim3((unsigned)((a->D + 255) / 256), (unsigned)a->n_seqs), 256, 0, st>>>(p, (int)a->n_seqs);
     });
@@ -531,8 +624,8 @@ int gdr_conv_step(const gdr_conv_step_args *a, void *stream) {
         return rc;
     if (!any) return GDR_OK;
     StepP p{a->x, a->weight, a->bias, a->state, a->y, a->slots, a->x_row, a->n_slots, (int)a->rows, (int)a->D, a->silu};
-    const bool vec = vec_ok(a->D, a->x_row, 0, a->dtype) && multiple16(a->x) && multiple16(a->weight) && multiple16(a->state) && multiple16(a->y);
-    const int cols = (int)((a->D + 7) / 8), threads = cols >= 128 ? 128 : (cols + 31) / 32 * 32;
+    const int vec = channels(a->D, {a->x_row}, a->dtype, a->weight, {a->x, a->state, a->y});
+    const int cols = (int)((a->D + vec - 1) / vec), threads = cols >= 128 ? 128 : (cols + 31) / 32 * 32;
     const dim3 grid((unsigned)((cols + threads - 1) / threads), (unsigned)a->rows);
     by_type(a->dtype, a->W, vec, [&](auto t, auto w, auto v) {
         k_conv_step<decltype(t), decltype(w)::value, decltype(v)::value><<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(p);

@@ -30,8 +30,7 @@ namespace {
 
 __device__ unsigned g_ssm_status;
 
-constexpr int kThreads = 128;          // scanning threads; as many help
-constexpr int kTile = 32;              // tokens staged at a time (forward)
+constexpr int kThreads = 128;          // scanning threads of a CTA
 constexpr int kBack = GDR_SSM_STRIDE;  // tokens of a backward tile, and between checkpoints
 constexpr int kGroup = 8;              // tokens of a backward tile whose latencies overlap
 
@@ -207,31 +206,35 @@ __device__ __forceinline__ float lane_sum(const float *p) {
     return (v.x + v.y) + (v.z + v.w);
 }
 
-// Forward, or (kSum) the segments' summaries.
-template <int kL, bool kSum>
+// Forward, or (kSum) the segments' summaries.  kHelp: groups of 128 helping
+// threads.  One where two CTAs share an SM; two (and tiles of 64 tokens) where
+// a CTA has an SM to itself: the helpers of 32 tokens take 0.84 us there, the
+// scan 0.75 us, each waiting on its own latencies.
+template <int kL, bool kSum, int kHelp>
 struct FwdSmem {
-    static constexpr int kCh = kThreads / kL, kN = 4 * kL;
+    static constexpr int kTile = 32 * kHelp, kCh = kThreads / kL, kN = 4 * kL;
     float2 in[2][kTile][kCh];  // s, s x
     float B[2][kTile][kN];
     float C[kSum ? 1 : 2][kTile][kN];
     float part[kSum ? 1 : 2][kTile][kCh][kL];  // C . h, a lane's part
 };
 
-template <typename T, int kL, bool kVec, bool kSum>
-__global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_fwd(const SsmP p) {
+template <typename T, int kL, bool kVec, bool kSum, int kHelp>
+__global__ void __launch_bounds__((1 + kHelp) * kThreads, kHelp == 1 ? 2 : 1) k_ssm_fwd(const SsmP p) {
     using W = Place<kL>;
-    constexpr int kCh = W::kCh, kN = W::kN;
+    using S = FwdSmem<kL, kSum, kHelp>;
+    constexpr int kCh = W::kCh, kN = W::kN, kTile = S::kTile, kHelpers = kHelp * kThreads;
     extern __shared__ __align__(16) char smem_raw[];
-    FwdSmem<kL, kSum> &sm = *reinterpret_cast<FwdSmem<kL, kSum> *>(smem_raw);
+    S &sm = *reinterpret_cast<S *>(smem_raw);
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_bounds(p.seqs, &g_ssm_status);
     const W w(p);
     const int seg = blockIdx.y, b = blockIdx.z;
     const int ts = seg * p.seg_len, te = min(ts + p.seg_len, p.T), tiles = (te - ts + kTile - 1) / kTile;
 
     if (threadIdx.x >= kThreads) {  // ---- the helpers
-        constexpr int kItems = kTile * kCh / 8, kNI = (kItems + kThreads - 1) / kThreads;  // 8 channels of a token each
-        constexpr int kBV = kTile * kN / 8, kNB = ((kSum ? 1 : 2) * kBV + kThreads - 1) / kThreads;
-        constexpr int kRows = kThreads / (kCh / 8);  // tokens from a thread's item to its next
+        constexpr int kItems = kTile * kCh / 8, kNI = (kItems + kHelpers - 1) / kHelpers;  // 8 channels of a token each
+        constexpr int kBV = kTile * kN / 8, kNB = ((kSum ? 1 : 2) * kBV + kHelpers - 1) / kHelpers;
+        constexpr int kRows = kHelpers / (kCh / 8);  // tokens from a thread's item to its next
         const int ht = threadIdx.x - kThreads;
         const int c = ht % (kCh / 8) * 8, row0 = ht / (kCh / 8), nv = min(8, w.nch - c);
         const T *x = static_cast<const T *>(p.x) + b * p.x_batch + w.c0 + c;
@@ -249,14 +252,14 @@ __global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_fwd(const SsmP p) {
         auto fetch = [&](int tb, Fetched &f) {
 #pragma unroll
             for (int i = 0; i < kNI; ++i) {
-                const int row = tb + row0 + i * kRows, n = ht + i * kThreads < kItems && row < te ? nv : 0;
+                const int row = tb + row0 + i * kRows, n = ht + i * kHelpers < kItems && row < te ? nv : 0;
                 f.x[i] = load8<T, kVec>(x + row * p.x_row, n);
                 f.dt[i] = load8<T, kVec>(dt + row * p.dt_row, n);
                 if (!kSum && z) f.z[i] = load8<T, kVec>(z + row * p.z_row, n);
             }
 #pragma unroll
             for (int i = 0; i < kNB; ++i) {
-                const int v = ht + i * kThreads, r = v % kBV, row = tb + r / (kN / 8), col = (r % (kN / 8)) * 8;
+                const int v = ht + i * kHelpers, r = v % kBV, row = tb + r / (kN / 8), col = (r % (kN / 8)) * 8;
                 const int n = v < (kSum ? 1 : 2) * kBV && row < te ? 8 : 0;
                 if (v >= kBV) f.bc[i] = load8<T, kVec>(Cm + row * p.c_row + col, n);
                 else f.bc[i] = load8<T, kVec>(Bm + row * p.b_row + col, n);
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_fwd(const SsmP p) {
         auto stage = [&](int tb, int buf, const Fetched &f) {
 #pragma unroll
             for (int i = 0; i < kNI; ++i) {
-                if (ht + i * kThreads >= kItems) continue;
+                if (ht + i * kHelpers >= kItems) continue;
                 const int row = row0 + i * kRows, key = pair_key<kCh>(row, c);
                 const bool real = tb + row < te;  // past the end: no decay, no input
                 f32x2 xv[4], dv[4];
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_fwd(const SsmP p) {
             }
 #pragma unroll
             for (int i = 0; i < kNB; ++i) {
-                const int v = ht + i * kThreads, r = v % kBV, row = r / (kN / 8), col = (r % (kN / 8)) * 8;
+                const int v = ht + i * kHelpers, r = v % kBV, row = r / (kN / 8), col = (r % (kN / 8)) * 8;
                 if (v >= (kSum ? 1 : 2) * kBV) continue;
                 float g[8];
                 unpack8(f.bc[i], g);
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_fwd(const SsmP p) {
 #pragma unroll
                 for (int j = 0; j < kNI; ++j) {
                     const int row = row0 + j * kRows, key = place_key<kCh>(row, c);
-                    if (ht + j * kThreads >= kItems || tp + row >= te || nv <= 0) continue;
+                    if (ht + j * kHelpers >= kItems || tp + row >= te || nv <= 0) continue;
                     f32x2 xv[4], zv[4], u[4];
                     get8(done.x[j], xv);
                     if (z) get8(done.z[j], zv);
@@ -898,21 +901,20 @@ struct SsmPlan {
     int tiles, S, seg_len;
 };
 
-// Segments: an estimate in cycles a token of a CTA.  A CTA alone on an SM
-// advances a token in about kLat cycles (its four warps wait on the chain of
-// decays); k of them share the SM's issue slots at about kThr each.
+// Segments: an estimate from measured times a token of a CTA (ns, N = 16):
+// forward 28 alone on an SM, else 26 times the CTAs of an SM; backward 160 and
+// 115; a summary pass 19 and 50 times the CTAs of an SM; and 6 us for the pass.
 SsmPlan ssm_plan(long long B, long long T, long long D, long long G, int N, bool bwd) {
     const int ch = kThreads / (N / 4);
     const long long tiles = (D / G + ch - 1) / ch, ctas = tiles * G * B, sms = layer_sms();
-    const double kLat = bwd ? 140 : 45, kThr = bwd ? 100 : 25, kSum = bwd ? 0.35 : 0.6;
+    const double one = bwd ? 160 : 28, more = bwd ? 115 : 26, sum = bwd ? 50 : 19;
+    auto load = [&](long long n) { return (double)((n + sms - 1) / sms); };
     double best = 1e300;
     int S = 1;
     for (int s = 1; s <= 64; ++s) {
-        if (s > 1 && (T / s < 64)) break;
-        const double tok = (double)((T + s - 1) / s);
-        const double per = std::max(kLat, kThr * (double)((ctas * s + sms - 1) / sms));
-        const double sum = s == 1 ? 0 : kSum * std::max(kLat, kThr * (double)((ctas * (s - 1) + sms - 1) / sms));
-        const double t = tok * (per + sum) + (s > 1 ? 6000 + 200.0 * s : 0);
+        if (s > 1 && T / s < 64) break;
+        const double tok = (double)((T + s - 1) / s), k = load(ctas * s);
+        const double t = tok * (std::max(one, more * k) + (s > 1 ? sum * load(ctas * (s - 1)) : 0)) + (s > 1 ? 6000 + 100.0 * s : 0);
         if (t < best * 0.999) {
             best = t;
             S = s;
@@ -1022,10 +1024,10 @@ int ssm_workspace(const gdr_ssm_args *a, size_t need, const char *what) {
 }
 
 template <typename K>
-int ssm_launch(K *kernel, size_t smem, dim3 grid, const SsmP &p, cudaStream_t st) {
+int ssm_launch(K *kernel, size_t smem, int threads, dim3 grid, const SsmP &p, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return layer_fail(GDR_ERR_CUDA, "scan: %s", cudaGetErrorString(e));
-    kernel<<<grid, 2 * kThreads, smem, st>>>(p);
+    kernel<<<grid, threads, smem, st>>>(p);
     return GDR_OK;
 }
 
@@ -1081,8 +1083,12 @@ int gdr_ssm_fwd(const gdr_ssm_args *a, void *stream) {
         constexpr bool V = decltype(v)::value;
         const unsigned gx = (unsigned)(pl.tiles * a->G), gz = (unsigned)a->B;
         rc = GDR_OK;
-        if (pl.S > 1) rc = ssm_launch(k_ssm_fwd<E, L, V, true>, sizeof(FwdSmem<L, true>), dim3(gx, pl.S - 1, gz), p, st);
-        if (!rc) rc = ssm_launch(k_ssm_fwd<E, L, V, false>, sizeof(FwdSmem<L, false>), dim3(gx, pl.S, gz), p, st);
+        if (pl.S > 1) rc = ssm_launch(k_ssm_fwd<E, L, V, true, 1>, sizeof(FwdSmem<L, true, 1>), 2 * kThreads, dim3(gx, pl.S - 1, gz), p, st);
+        if (rc) return;
+        if ((long long)gx * pl.S * gz <= layer_sms())
+            rc = ssm_launch(k_ssm_fwd<E, L, V, false, 2>, sizeof(FwdSmem<L, false, 2>), 3 * kThreads, dim3(gx, pl.S, gz), p, st);
+        else
+            rc = ssm_launch(k_ssm_fwd<E, L, V, false, 1>, sizeof(FwdSmem<L, false, 1>), 2 * kThreads, dim3(gx, pl.S, gz), p, st);
     });
     return rc ? rc : layer_launched("scan forward");
 }
@@ -1120,8 +1126,8 @@ int gdr_ssm_bwd(const gdr_ssm_args *a, void *stream) {
         constexpr bool V = decltype(v)::value;
         const unsigned gx = (unsigned)(pl.tiles * a->G), gz = (unsigned)a->B;
         rc = GDR_OK;
-        if (pl.S > 1) rc = ssm_launch(k_ssm_bwd<E, L, V, true>, sizeof(BwdSmem<L, true>), dim3(gx, pl.S - 1, gz), p, st);
-        if (!rc) rc = ssm_launch(k_ssm_bwd<E, L, V, false>, sizeof(BwdSmem<L, false>), dim3(gx, pl.S, gz), p, st);
+        if (pl.S > 1) rc = ssm_launch(k_ssm_bwd<E, L, V, true>, sizeof(BwdSmem<L, true>), 2 * kThreads, dim3(gx, pl.S - 1, gz), p, st);
+        if (!rc) rc = ssm_launch(k_ssm_bwd<E, L, V, false>, sizeof(BwdSmem<L, false>), 2 * kThreads, dim3(gx, pl.S, gz), p, st);
         if (!rc) k_ssm_bwd_sum<E><<<(unsigned)((outs + 255) / 256), 256, 0, st>>>(p, a->N);
     });
     return rc ? rc : layer_launched("scan backward");
