@@ -7,11 +7,19 @@
 // Bound by memory: a row is read once into the registers of one CTA, reduced
 // once, and written once.  The norm is taken of r as it is stored, so that
 // the gradient, which reads the stored r, is that of what was computed.
+//
+// Accesses are of eight elements.  Where a row's length is not a multiple of
+// eight, rows begin inside one; there (kShift) a thread's eight channels are
+// those of an aligned piece of memory.  A row's first and last piece then
+// reaches into its neighbours: it is read whole all the same and cut in
+// registers (element by element only at the end of the tensor), and written
+// element by element.
 #include "gdr_layer.h"
 
 namespace {
 
-constexpr int kMaxThreads = 512, kMaxIter = 4;  // 8 x 512 x 4 channels a row
+constexpr int kMaxThreads = 544, kMaxIter = 4;  // 8 x 512 x 4 channels a row, and a piece more where shifted
+constexpr int kMaxD = 8 * 512 * 4;
 
 struct NormP {
     const void *x, *residual;
@@ -22,7 +30,81 @@ struct NormP {
     long long M, x_row, r_row;
     int D;
     float eps;
+    bool x_vec, r_vec, o_vec;  // kShift: pieces of x, residual and the outputs are aligned
 };
+
+// Channels c .. c + 7 of a row of D, of which [lo, hi) exist.
+struct Piece {
+    int c, lo, hi;
+    __device__ __forceinline__ Piece(int c_, int D) : c(c_), lo(max(0, -c_)), hi(min(8, D - c_)) {}
+    __device__ __forceinline__ bool whole() const { return lo == 0 && hi == 8; }
+};
+// vec: pieces are aligned; inner: what lies up to seven elements around the row
+// is the tensor's too.
+template <typename T, bool kShift>
+__device__ __forceinline__ Raw8<T> load_piece(const T *row, const Piece &k, bool vec, bool inner) {
+    if (!kShift) return load8<T, true>(row + k.c, k.hi);
+    if (vec && (k.whole() || inner)) return load8<T, true>(row + k.c, k.hi > 0 ? 8 : 0);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = e >= k.lo && e < k.hi ? to_f(row[k.c + e]) : 0.f;
+    Raw8<T> r;
+    pack8(f, r);
+    return r;
+}
+template <bool kShift, typename R>
+__device__ __forceinline__ void unpack_piece(const R &r, const Piece &k, float (&f)[8]) {
+    unpack8(r, f);
+    if (kShift && !k.whole())
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < k.lo || e >= k.hi) f[e] = 0.f;
+}
+template <typename T, bool kShift>
+__device__ __forceinline__ void store_piece(T *row, const Piece &k, const float (&f)[8], bool vec) {
+    if (!kShift) {
+        store8<T, true>(row + k.c, f, k.hi);
+    } else if (k.whole() && vec) {
+        store8<T, true>(row + k.c, f, 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e >= k.lo && e < k.hi) from_f(row[k.c + e], f[e]);
+    }
+}
+template <int kBy>
+__device__ __forceinline__ void pick8(const float (&win)[16], float (&f)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = win[8 - kBy + e];
+}
+// The weights of a piece.  Shifted ones are cut from sixteen aligned ones (the
+// shift is the row's, the same for all threads): eight scalar reads a thread
+// touch eight times the lines.
+template <bool kShift>
+__device__ __forceinline__ void load_weight(const float *w, const Piece &k, int D, float (&f)[8]) {
+    const int base = (k.c + 7) & ~7, shift = base - k.c;  // a multiple of eight
+    if (!kShift && k.hi > 0) {
+        *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(w + k.c);
+        *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(w + k.c + 4);
+    } else if (kShift && base >= 8 && base + 8 <= D && !(reinterpret_cast<uintptr_t>(w) & 15u)) {
+        float win[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(win + 4 * i) = *reinterpret_cast<const float4 *>(w + base - 8 + 4 * i);
+        switch (shift) {
+            case 0: pick8<0>(win, f); break;
+            case 1: pick8<1>(win, f); break;
+            case 2: pick8<2>(win, f); break;
+            case 3: pick8<3>(win, f); break;
+            case 4: pick8<4>(win, f); break;
+            case 5: pick8<5>(win, f); break;
+            case 6: pick8<6>(win, f); break;
+            default: pick8<7>(win, f); break;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = kShift && e >= k.lo && e < k.hi ? w[k.c + e] : 0.f;
+    }
+}
 
 // Sum of (up to two) values over the CTA; `buf` alternates between calls so
 // that one barrier a call is enough.
@@ -58,31 +140,34 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-template <typename T, int kIter, bool kVec, bool kQuant>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_fwd(const NormP p) {
+template <typename T, int kIter, bool kShift, bool kQuant>
+__global__ void __launch_bounds__(kIter == 4 ? kMaxThreads : 512, kIter == 4 ? 1 : 3) k_norm_fwd(const NormP p) {
     __shared__ float2 buf[32];
-    const long long row = blockIdx.x;
+    __shared__ unsigned tops[kShift && kQuant ? 128 : 1];  // greatest magnitudes of the row's blocks, as ordered bits
+    const long long row = blockIdx.x, out = row * p.D;
+    const int shift = kShift ? (int)(out & 7) : 0;
     const T *x = static_cast<const T *>(p.x) + row * p.x_row;
     const T *res = p.residual ? static_cast<const T *>(p.residual) + row * p.r_row : nullptr;
-    const long long out = row * p.D;
+    if (kShift && kQuant)
+        for (int i = threadIdx.x; i < 128; i += blockDim.x) tops[i] = 0;
+    auto piece = [&](int i) { return Piece((int)(threadIdx.x + i * blockDim.x) * 8 - shift, p.D); };
     Raw8<T> rx[kIter], rr[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * 8, n = min(8, p.D - c);
-        rx[i] = load8<T, kVec>(x + c, n);
-        if (res) rr[i] = load8<T, kVec>(res + c, n);
+        const Piece k = piece(i);
+        rx[i] = load_piece<T, kShift>(x, k, p.x_vec, row + 1 < p.M && p.x_row >= p.D);
+        if (res) rr[i] = load_piece<T, kShift>(res, k, p.r_vec, row + 1 < p.M && p.r_row >= p.D);
     }
     float v[kIter][8], sq = 0.f;
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * 8, n = min(8, p.D - c);
-        unpack8(rx[i], v[i]);
+        unpack_piece<kShift>(rx[i], piece(i), v[i]);
         if (res) {
             float f[8];
-            unpack8(rr[i], f);
+            unpack_piece<kShift>(rr[i], piece(i), f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[i][e] += f[e];
-            store8<T, kVec>(static_cast<T *>(p.sum) + out + c, v[i], n);
+            store_piece<T, kShift>(static_cast<T *>(p.sum) + out, piece(i), v[i], p.o_vec);
             Raw8<T> stored;
             pack8(v[i], stored);
             unpack8(stored, v[i]);
@@ -93,28 +178,64 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_fwd(const NormP p) {
     const float rstd = 1.f / sqrtf(cta_sum(sq, 0.f, buf).x / (float)p.D + p.eps);
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * 8, n = min(8, p.D - c);
+        const Piece k = piece(i);
+        float w[8];
+        load_weight<kShift>(p.weight, k, p.D, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = e < n ? v[i][e] * rstd * p.weight[c + e] : 0.f;
+        for (int e = 0; e < 8; ++e) v[i][e] = e >= k.lo && e < k.hi ? v[i][e] * rstd * w[e] : 0.f;
         if (!kQuant) {
-            store8<T, kVec>(static_cast<T *>(p.y) + out + c, v[i], n);
-            continue;
-        }
-        // 16 neighbouring threads hold a block of 128 channels
-        float top = 0.f;
+            store_piece<T, kShift>(static_cast<T *>(p.y) + out, k, v[i], p.o_vec);
+        } else if (kShift) {
+            // a piece may lie in two blocks of 128, a warp's pieces in three
+            const int b0 = max(k.c, 0) / 128;
+            unsigned mine[2] = {0, 0};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(v[i][e]));
+            for (int e = 0; e < 8; ++e) {
+                const unsigned bits = __float_as_uint(fabsf(v[i][e]));  // NaN above all
+                if ((k.c + e) / 128 == b0 || k.c + e < 0) mine[0] = max(mine[0], bits);
+                else mine[1] = max(mine[1], bits);
+            }
+            const int first = max(__shfl_sync(0xffffffffu, k.c, 0), 0) / 128;
 #pragma unroll
-        for (int m = 8; m >= 1; m /= 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, m));
-        const float scale = max_nan(top, 1e-30f) / 448.f, inv = 1.f / scale;
-        if (n <= 0) continue;
-        if (threadIdx.x % 16 == 0) p.scales[(long long)(c / 128) * p.M + row] = scale;
-        const uint32_t lo = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-        const uint32_t hi = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
-        if (kVec) {
-            *reinterpret_cast<uint2 *>(p.q + out + c) = make_uint2(lo, hi);
+            for (int b = 0; b < 3; ++b) {
+                const unsigned top = __reduce_max_sync(0xffffffffu, first + b == b0 ? mine[0] : first + b == b0 + 1 ? mine[1] : 0u);
+                if (threadIdx.x % 32 == 0 && top && first + b < 128) atomicMax(&tops[first + b], top);
+            }
         } else {
-            for (int e = 0; e < n; ++e) p.q[out + c + e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
+            // 16 neighbouring threads hold a block of 128 channels
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(v[i][e]));
+#pragma unroll
+            for (int m = 8; m >= 1; m /= 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, m));
+            const float scale = max_nan(top, 1e-30f) / 448.f, inv = 1.f / scale;
+            if (k.hi <= 0) continue;
+            if (threadIdx.x % 16 == 0) p.scales[(long long)(k.c / 128) * p.M + row] = scale;
+            *reinterpret_cast<uint2 *>(p.q + out + k.c) =
+                make_uint2(e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
+                           e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv));
+        }
+    }
+    if (!kShift || !kQuant) return;
+    __syncthreads();
+    auto scale_of = [&](int b) { return max_nan(__uint_as_float(tops[b]), 1e-30f) / 448.f; };
+    for (int b = threadIdx.x; b < (p.D + 127) / 128; b += blockDim.x) p.scales[(long long)b * p.M + row] = scale_of(b);
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+        const Piece k = piece(i);
+        if (k.hi <= 0) continue;
+        const int b0 = max(k.c, 0) / 128, b1 = min(k.c + 7, p.D - 1) / 128;
+        const float i0 = 1.f / scale_of(b0), i1 = b1 == b0 ? i0 : 1.f / scale_of(b1);
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = v[i][e] * (k.c + e >= b1 * 128 ? i1 : i0);
+        const uint32_t lo = e4m3x4(o[0], o[1], o[2], o[3]), hi = e4m3x4(o[4], o[5], o[6], o[7]);
+        if (k.whole() && p.o_vec) {
+            *reinterpret_cast<uint2 *>(p.q + out + k.c) = make_uint2(lo, hi);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e >= k.lo && e < k.hi) p.q[out + k.c + e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
         }
     }
 }
@@ -127,12 +248,16 @@ struct NormBwdP {
     long long M;
     int D;
     float eps;
+    bool vec;  // kShift: pieces are aligned
 };
 
-// A CTA takes every gridDim-th row and keeps its part of dweight in registers.
-template <typename T, int kIter, bool kVec>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_bwd(const NormBwdP p) {
+// A CTA takes every gridDim-th row and keeps its part of dweight in registers
+// (kShift: gridDim is a multiple of eight, so that its rows begin alike).
+template <typename T, int kIter, bool kShift>
+__global__ void __launch_bounds__(kIter == 4 ? kMaxThreads : 512) k_norm_bwd(const NormBwdP p) {
     __shared__ float2 buf[2][32];
+    const int shift = kShift ? (int)(((long long)blockIdx.x * p.D) & 7) : 0;
+    auto piece = [&](int i) { return Piece((int)(threadIdx.x + i * blockDim.x) * 8 - shift, p.D); };
     float gw[kIter][8];
 #pragma unroll
     for (int i = 0; i < kIter; ++i)
@@ -144,48 +269,49 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_bwd(const NormBwdP p) {
         Raw8<T> rr[kIter], rg[kIter], rs[kIter];
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-            const int c = (threadIdx.x + i * blockDim.x) * 8, n = min(8, p.D - c);
-            rr[i] = load8<T, kVec>(static_cast<const T *>(p.r) + at + c, n);
-            rg[i] = load8<T, kVec>(static_cast<const T *>(p.dy) + at + c, n);
-            if (p.dsum) rs[i] = load8<T, kVec>(static_cast<const T *>(p.dsum) + at + c, n);
+            const Piece k = piece(i);
+            const bool inner = row + 1 < p.M;
+            rr[i] = load_piece<T, kShift>(static_cast<const T *>(p.r) + at, k, p.vec, inner);
+            rg[i] = load_piece<T, kShift>(static_cast<const T *>(p.dy) + at, k, p.vec, inner);
+            if (p.dsum) rs[i] = load_piece<T, kShift>(static_cast<const T *>(p.dsum) + at, k, p.vec, inner);
         }
         float sq = 0.f, gr = 0.f;
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-            const int c = (threadIdx.x + i * blockDim.x) * 8, n = min(8, p.D - c);
-            float r[8], g[8];
-            unpack8(rr[i], r);
-            unpack8(rg[i], g);
+            float r[8], g[8], w[8];
+            unpack_piece<kShift>(rr[i], piece(i), r);
+            unpack_piece<kShift>(rg[i], piece(i), g);
+            load_weight<kShift>(p.weight, piece(i), p.D, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 sq = fmaf(r[e], r[e], sq);
-                gr = fmaf(e < n ? g[e] * p.weight[c + e] : 0.f, r[e], gr);
+                gr = fmaf(g[e] * w[e], r[e], gr);
             }
         }
         const float2 s = cta_sum(sq, gr, buf[turn]);
-        const float rstd = 1.f / sqrtf(s.x / (float)p.D + p.eps), k = rstd * rstd * s.y / (float)p.D;
+        const float rstd = 1.f / sqrtf(s.x / (float)p.D + p.eps), m = rstd * rstd * s.y / (float)p.D;
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-            const int c = (threadIdx.x + i * blockDim.x) * 8, n = min(8, p.D - c);
-            float r[8], g[8], o[8];
-            unpack8(rr[i], r);
-            unpack8(rg[i], g);
+            const Piece k = piece(i);
+            float r[8], g[8], o[8], w[8];
+            unpack_piece<kShift>(rr[i], k, r);
+            unpack_piece<kShift>(rg[i], k, g);
             if (p.dsum) unpack8(rs[i], o);
+            load_weight<kShift>(p.weight, k, p.D, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float gv = e < n ? g[e] * p.weight[c + e] : 0.f;
-                o[e] = fmaf(rstd, gv - r[e] * k, p.dsum ? o[e] : 0.f);
+                o[e] = fmaf(rstd, g[e] * w[e] - r[e] * m, p.dsum ? o[e] : 0.f);
                 gw[i][e] = fmaf(g[e], r[e] * rstd, gw[i][e]);
             }
-            store8<T, kVec>(static_cast<T *>(p.dr) + at + c, o, n);
+            store_piece<T, kShift>(static_cast<T *>(p.dr) + at, k, o, p.vec);
         }
     }
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        const Piece k = piece(i);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (c + e < p.D) p.part[(long long)blockIdx.x * p.D + c + e] = gw[i][e];
+            if (e >= k.lo && e < k.hi) p.part[(long long)blockIdx.x * p.D + k.c + e] = gw[i][e];
     }
 }
 
@@ -206,7 +332,7 @@ __global__ void __launch_bounds__(1024) k_norm_bwd_sum(const float *part, int ro
 
 int norm_sizes(long long M, long long D, int dtype) {
     if (M < 0 || D < 1) return layer_fail(GDR_ERR_SHAPE, "norm: M must be >= 0 and D >= 1 (got %lld, %lld)", M, D);
-    if (D > 8LL * kMaxThreads * kMaxIter) return layer_fail(GDR_ERR_SHAPE, "norm: D must be at most %d (got %lld)", 8 * kMaxThreads * kMaxIter, D);
+    if (D > kMaxD) return layer_fail(GDR_ERR_SHAPE, "norm: D must be at most %d (got %lld)", kMaxD, D);
     if (M >= (1LL << 31)) return layer_fail(GDR_ERR_SHAPE, "norm: too many rows");
     if (dtype != GDR_BF16 && dtype != GDR_F32) return layer_fail(GDR_ERR_DTYPE, "norm: unknown dtype %d", dtype);
     return GDR_OK;
@@ -214,26 +340,27 @@ int norm_sizes(long long M, long long D, int dtype) {
 
 // Two or more 8-channel vectors a thread where a row has them: the row's loads
 // are in flight together.
-void shape_of(long long D, int *threads, int *iter) {
-    const int vecs = (int)((D + 7) / 8);
-    int t = std::min(kMaxThreads, std::max(32, ((vecs + 1) / 2 + 31) / 32 * 32));
+void shape_of(long long D, bool shift, int *threads, int *iter) {
+    const int vecs = (int)((D + (shift ? 14 : 7)) / 8);  // a shifted row may need a piece more
+    int t = std::min(512, std::max(32, ((vecs + 1) / 2 + 31) / 32 * 32));
     *threads = t;
+    if (vecs > t * kMaxIter) t += 32;
     const int need = (vecs + t - 1) / t;
     *iter = need <= 1 ? 1 : need <= 2 ? 2 : 4;
 }
 
 int bwd_ctas(long long M, long long D) {
     int threads, iter;
-    shape_of(D, &threads, &iter);
-    const long long per_sm = std::max(1, std::min(16, 1024 / threads));
-    return (int)std::max(1LL, std::min(M, per_sm * layer_sms()));
+    shape_of(D, true, &threads, &iter);
+    const long long per_sm = std::max(1, std::min(16, 768 / threads));
+    return (int)((std::max(1LL, std::min(M, per_sm * layer_sms())) + 7) / 8 * 8);
 }
 
 template <typename F>
-void norm_by_type(int dtype, int iter, bool vec, F f) {
+void norm_by_type(int dtype, int iter, bool shift, F f) {
     auto w = [&](auto t) {
         auto v = [&](auto l) {
-            if (vec) f(t, l, std::true_type{}); else f(t, l, std::false_type{});
+            if (shift) f(t, l, std::true_type{}); else f(t, l, std::false_type{});
         };
         if (iter == 1) v(std::integral_constant<int, 1>{});
         else if (iter == 2) v(std::integral_constant<int, 2>{});
@@ -258,13 +385,16 @@ int gdr_norm_fwd(const gdr_norm_args *a, void *stream) {
         (rc = layer_ptr("y", a->y, false, e)) || (rc = layer_ptr("scales", a->scales, any && a->q, 4)))
         return rc;
     if (!any) return GDR_OK;
-    NormP p{a->x, a->residual, a->weight, a->sum, a->y, static_cast<uint8_t *>(a->q), a->scales, a->M, a->x_row, a->r_row, (int)a->D, a->eps};
-    const long long q = a->dtype == GDR_BF16 ? 8 : 4;
-    const bool vec = a->D % 8 == 0 && a->x_row % q == 0 && (!a->residual || a->r_row % q == 0) && multiple16(a->x) &&
-                     multiple16(a->residual) && multiple16(a->sum) && multiple16(a->y) && multiple16(a->q);
+    NormP p{a->x, a->residual, a->weight, a->sum, a->y, static_cast<uint8_t *>(a->q), a->scales, a->M, a->x_row, a->r_row, (int)a->D, a->eps, true, true, true};
+    // rows of a tensor begin as the outputs' do
+    auto alike = [&](const void *t, long long row) { return !t || (multiple16(t) && (row - a->D) % 8 == 0); };
+    p.x_vec = alike(a->x, a->x_row);
+    p.r_vec = alike(a->residual, a->r_row);
+    p.o_vec = multiple16(a->sum) && multiple16(a->y) && multiple16(a->q);
+    const bool shift = a->D % 8 || !p.x_vec || !p.r_vec || !p.o_vec || !multiple16(a->weight);
     int threads, iter;
-    shape_of(a->D, &threads, &iter);
-    norm_by_type(a->dtype, iter, vec, [&](auto t, auto l, auto v) {
+    shape_of(a->D, shift, &threads, &iter);
+    norm_by_type(a->dtype, iter, shift, [&](auto t, auto l, auto v) {
         using E = decltype(t);
         constexpr int I = decltype(l)::value;
         constexpr bool V = decltype(v)::value;
@@ -295,12 +425,13 @@ int gdr_norm_bwd(const gdr_norm_bwd_args *a, void *stream) {
     if (a->workspace_bytes < gdr_norm_bwd_workspace_size(a->M, a->D))
         return layer_fail(GDR_ERR_WORKSPACE, "norm backward: workspace too small");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    NormBwdP p{a->r, a->dy, a->dsum, a->weight, a->dr, static_cast<float *>(a->workspace), a->dweight, a->M, (int)a->D, a->eps};
-    const bool vec = a->D % 8 == 0 && multiple16(a->r) && multiple16(a->dy) && multiple16(a->dsum) && multiple16(a->dr);
+    NormBwdP p{a->r, a->dy, a->dsum, a->weight, a->dr, static_cast<float *>(a->workspace), a->dweight, a->M, (int)a->D, a->eps, true};
+    p.vec = multiple16(a->r) && multiple16(a->dy) && multiple16(a->dsum) && multiple16(a->dr);
+    const bool shift = a->D % 8 || !p.vec || !multiple16(a->weight);
     int threads, iter;
-    shape_of(a->D, &threads, &iter);
+    shape_of(a->D, shift, &threads, &iter);
     const int ctas = bwd_ctas(a->M, a->D);
-    norm_by_type(a->dtype, iter, vec, [&](auto t, auto l, auto v) {
+    norm_by_type(a->dtype, iter, shift, [&](auto t, auto l, auto v) {
         k_norm_bwd<decltype(t), decltype(l)::value, decltype(v)::value><<<ctas, threads, 0, st>>>(p);
     });
     k_norm_bwd_sum<<<(unsigned)((a->D + 31) / 32), dim3(32, 32), 0, st>>>(p.part, ctas, (int)a->D, a->dweight);
