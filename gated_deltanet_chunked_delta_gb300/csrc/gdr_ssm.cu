@@ -135,6 +135,63 @@ __device__ __forceinline__ State load_A2(const SsmP &p, const Place<kL> &w, Stat
     return State{mul2(a.a, k), mul2(a.b, k)};
 }
 
+// Eight neighbouring elements on their way.  Where rows are not 16-byte
+// aligned (odd widths) the aligned 16-byte pieces that hold them are read (each
+// holds at least one of them, so none leaves the tensor's memory) and the
+// elements are cut out once they have arrived.
+template <typename T, bool kVec>
+struct Flight {
+    static constexpr int kPieces = sizeof(T) / 2 + (kVec ? 0 : 1);
+    uint4 w[kPieces];
+    int off, n;
+    __device__ __forceinline__ void fetch(const T *p, int count) {  // count elements exist, at most eight
+        if (kVec) {
+            const Raw8<T> r = load8<T, true>(p, count);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) w[i] = r.w[i];
+            return;
+        }
+        n = min(count, 8);
+        off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        const uint4 *base = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            w[i] = 16 * i < off + n * (int)sizeof(T) && n > 0 ? base[i] : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ Raw8<T> land() const {
+        Raw8<T> r;
+        if (kVec) {
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = w[i];
+            return r;
+        }
+        constexpr int kW = 4 * kPieces, kOut = 2 * sizeof(T);
+        uint32_t v[kW + 3];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            v[4 * i] = w[i].x; v[4 * i + 1] = w[i].y; v[4 * i + 2] = w[i].z; v[4 * i + 3] = w[i].w;
+        }
+        v[kW] = v[kW + 1] = v[kW + 2] = 0;
+#pragma unroll
+        for (int i = 0; i < kOut + 2; ++i) v[i] = off & 8 ? v[i + 2] : v[i];
+#pragma unroll
+        for (int i = 0; i < kOut + 1; ++i) v[i] = off & 4 ? v[i + 1] : v[i];
+        if (sizeof(T) == 2)
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) v[i] = off & 2 ? __funnelshift_r(v[i], v[i + 1], 16) : v[i];
+        if (n < 8)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e >= n) {
+                    if (sizeof(T) == 2) v[e / 2] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                    else v[e] = 0;
+                }
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        return r;
+    }
+};
+
 // Eight neighbouring channels of one token as packed pairs.
 template <typename T>
 __device__ __forceinline__ void get8(const Raw8<T> &r, f32x2 (&v)[4]) {
@@ -249,20 +306,34 @@ __global__ void __launch_bounds__((1 + kHelp) * kThreads, kHelp == 1 ? 2 : 1) k_
         struct Fetched {
             Raw8<T> x[kNI], dt[kNI], z[kNI], bc[kNB];
         };
-        auto fetch = [&](int tb, Fetched &f) {
+        struct Flying {
+            Flight<T, kVec> x[kNI], dt[kNI], z[kNI], bc[kNB];
+        };
+        auto land = [&](const Flying &f) {
+            Fetched g;
+#pragma unroll
+            for (int i = 0; i < kNI; ++i) {
+                g.x[i] = f.x[i].land();
+                g.dt[i] = f.dt[i].land();
+                if (!kSum && z) g.z[i] = f.z[i].land();
+            }
+#pragma unroll
+            for (int i = 0; i < kNB; ++i) g.bc[i] = f.bc[i].land();
+            return g;
+        };
+        auto fetch = [&](int tb, Flying &f) {
 #pragma unroll
             for (int i = 0; i < kNI; ++i) {
                 const int row = tb + row0 + i * kRows, n = ht + i * kHelpers < kItems && row < te ? nv : 0;
-                f.x[i] = load8<T, kVec>(x + row * p.x_row, n);
-                f.dt[i] = load8<T, kVec>(dt + row * p.dt_row, n);
-                if (!kSum && z) f.z[i] = load8<T, kVec>(z + row * p.z_row, n);
+                f.x[i].fetch(x + row * p.x_row, n);
+                f.dt[i].fetch(dt + row * p.dt_row, n);
+                if (!kSum && z) f.z[i].fetch(z + row * p.z_row, n);
             }
 #pragma unroll
             for (int i = 0; i < kNB; ++i) {
                 const int v = ht + i * kHelpers, r = v % kBV, row = tb + r / (kN / 8), col = (r % (kN / 8)) * 8;
                 const int n = v < (kSum ? 1 : 2) * kBV && row < te ? 8 : 0;
-                if (v >= kBV) f.bc[i] = load8<T, kVec>(Cm + row * p.c_row + col, n);
-                else f.bc[i] = load8<T, kVec>(Bm + row * p.b_row + col, n);
+                f.bc[i].fetch(v >= kBV ? Cm + row * p.c_row + col : Bm + row * p.b_row + col, n);
             }
         };
         auto stage = [&](int tb, int buf, const Fetched &f) {
@@ -298,10 +369,13 @@ __global__ void __launch_bounds__((1 + kHelp) * kThreads, kHelp == 1 ? 2 : 1) k_
         };
         // Tiles in flight: the one to finish, the one being scanned, the one to
         // stage, and the one being fetched.
-        Fetched done, now, next, then;
-        fetch(ts, now);
-        if (tiles > 1) fetch(ts + kTile, next);
+        Fetched done, now, next;
+        Flying then;
+        fetch(ts, then);
+        now = land(then);
+        if (tiles > 1) fetch(ts + kTile, then);
         stage(ts, 0, now);
+        next = land(then);
         __syncthreads();
         for (int i = 0; i <= tiles; ++i) {
             if (i + 2 < tiles) fetch(ts + (i + 2) * kTile, then);
@@ -326,7 +400,7 @@ __global__ void __launch_bounds__((1 + kHelp) * kThreads, kHelp == 1 ? 2 : 1) k_
             }
             done = now;
             now = next;
-            next = then;
+            next = land(then);
             if (i < tiles) __syncthreads();
         }
         return;
@@ -445,7 +519,7 @@ __device__ __forceinline__ void put_fold(float *to, float2 v) {
 }
 
 template <typename T, int kL, bool kVec, bool kSum>
-__global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_bwd(const SsmP p) {
+__global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) k_ssm_bwd(const SsmP p) {
     using W = Place<kL>;
     using S = BwdSmem<kL, kSum>;
     constexpr int kCh = W::kCh, kN = W::kN;
@@ -477,24 +551,36 @@ __global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_bwd(const SsmP p) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) gskip[k] = gbias[k] = dup(0.f);
         struct Fetched {
-            Raw8<T> x[kNI], g[kNI], bc[kNB];  // x; dt, or dy
-            Raw8<T> z[kNI];
+            Raw8<T> x[kNI], g[kNI], z[kNI], bc[kNB];  // g: dt, or dy
         };
-        auto fetch = [&](int tb, Fetched &f) {
+        struct Flying {
+            Flight<T, kVec> x[kNI], g[kNI], z[kNI], bc[kNB];
+        };
+        auto land = [&](const Flying &f) {
+            Fetched r;
+#pragma unroll
+            for (int i = 0; i < kNI; ++i) {
+                r.x[i] = f.x[i].land();
+                r.g[i] = f.g[i].land();
+                if (z) r.z[i] = f.z[i].land();
+            }
+#pragma unroll
+            for (int i = 0; i < kNB; ++i) r.bc[i] = f.bc[i].land();
+            return r;
+        };
+        auto fetch = [&](int tb, Flying &f) {
 #pragma unroll
             for (int i = 0; i < kNI; ++i) {
                 const int v = ht + i * kThreads, t = tb + row, n = v < 2 * kPer && t < te ? nv : 0;
-                f.x[i] = load8<T, kVec>(x + t * p.x_row, n);
-                if (v < kPer) f.g[i] = load8<T, kVec>(dt + t * p.dt_row, n);
-                else f.g[i] = load8<T, kVec>(dy + (long long)t * p.D, n);
-                if (z && v >= kPer) f.z[i] = load8<T, kVec>(z + t * p.z_row, n);
+                f.x[i].fetch(x + t * p.x_row, n);
+                f.g[i].fetch(v < kPer ? dt + t * p.dt_row : dy + (long long)t * p.D, n);
+                if (z) f.z[i].fetch(z + t * p.z_row, v >= kPer ? n : 0);
             }
 #pragma unroll
             for (int i = 0; i < kNB; ++i) {
                 const int v = ht + i * kThreads, r = v % kBV, t = tb + r / (kN / 8), col = (r % (kN / 8)) * 8;
                 const int n = v < 2 * kBV && t < te ? 8 : 0;
-                if (v >= kBV) f.bc[i] = load8<T, kVec>(Cm + t * p.c_row + col, n);
-                else f.bc[i] = load8<T, kVec>(Bm + t * p.b_row + col, n);
+                f.bc[i].fetch(v >= kBV ? Cm + t * p.c_row + col : Bm + t * p.b_row + col, n);
             }
         };
         auto stage = [&](int tb, int buf, const Fetched &f) {
@@ -546,10 +632,13 @@ __global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_bwd(const SsmP p) {
             }
         };
         const int last = ts + (tiles - 1) * kBack;
-        Fetched done, now, next, then;  // as in the forward
-        fetch(last, now);
-        if (tiles > 1) fetch(last - kBack, next);
+        Fetched done, now, next;  // as in the forward
+        Flying then;
+        fetch(last, then);
+        now = land(then);
+        if (tiles > 1) fetch(last - kBack, then);
         stage(last, 0, now);
+        next = land(then);
         __syncthreads();
         for (int i = 0; i <= tiles; ++i) {
             if (i + 2 < tiles) fetch(last - (i + 2) * kBack, then);
@@ -615,7 +704,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) k_ssm_bwd(const SsmP p) {
             if (i + 1 < tiles) stage(last - (i + 1) * kBack, (i + 1) & 1, next);
             done = now;
             now = next;
-            next = then;
+            next = land(then);
             if (i < tiles) __syncthreads();
         }
         if (kSum) return;
@@ -840,7 +929,7 @@ struct StepP {
     const int32_t *slots;
     void *y;
     long long x_row, dt_row, z_row, b_row, c_row, n_slots;
-    int D, Dg, softplus;
+    int D, Dg, softplus, rows;
 };
 
 template <typename T>
@@ -848,40 +937,54 @@ __device__ __forceinline__ State four(const T *p) {
     return State{mk2(to_f(p[0]), to_f(p[1])), mk2(to_f(p[2]), to_f(p[3]))};
 }
 
-// Bound by memory: the states of the rows are read and written once.
-template <typename T, int kL>
+// Bound by memory: the states of the rows are read and written once.  A lane
+// has four states of a channel, of kRows rows at a time, so that their reads
+// are in flight together and the channel's parameters are read once.
+template <typename T, int kL, int kRows>
 __global__ void __launch_bounds__(kThreads) k_ssm_step(const StepP p) {
     constexpr int kCh = kThreads / kL, kN = 4 * kL;
-    const int r = blockIdx.y, d = blockIdx.x * kCh + threadIdx.x / kL, q = threadIdx.x % kL;
-    const long long slot = p.slots ? p.slots[r] : r;
-    const bool known = slot >= 0 && slot < p.n_slots, on = d < p.D;
-    if (slot >= p.n_slots && threadIdx.x == 0) atomicOr(&g_ssm_status, kStatusIndex);
-    float u = 0.f, xv = 0.f;
-    if (on && known) {
-        float *st = p.state + (slot * p.D + d) * kN + 4 * q;
-        const State h0 = load_state(st), A = load_state(p.A + (long long)d * kN + 4 * q);
-        const int g = d / p.Dg;
-        const State Bt = four(static_cast<const T *>(p.Bm) + r * p.b_row + g * kN + 4 * q);
-        const State Ct = four(static_cast<const T *>(p.Cm) + r * p.c_row + g * kN + 4 * q);
-        xv = to_f(static_cast<const T *>(p.x)[r * p.x_row + d]);
-        const float raw = to_f(static_cast<const T *>(p.dt)[r * p.dt_row + d]) + (p.dt_bias ? p.dt_bias[d] : 0.f);
-        const float s = p.softplus ? softplusf(raw) : raw;
-        const f32x2 k = mk2(kLog2e, kLog2e);
-        const State h = advance(decay(State{mul2(A.a, k), mul2(A.b, k)}, dup(s)), h0, dup(s * xv), Bt);
-        store_state(st, h);
-        u = dot(h, Ct);
+    const int d = blockIdx.x * kCh + threadIdx.x / kL, q = threadIdx.x % kL, r0 = blockIdx.y * kRows;
+    const bool on = d < p.D;
+    float *st[kRows];
+    State h[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = r0 + i;
+        const long long slot = r >= p.rows ? -1 : p.slots ? p.slots[r] : r;
+        if (slot >= p.n_slots && threadIdx.x == 0) atomicOr(&g_ssm_status, kStatusIndex);
+        st[i] = on && slot >= 0 && slot < p.n_slots ? p.state + (slot * p.D + d) * kN + 4 * q : nullptr;
     }
 #pragma unroll
-    for (int m = kL / 2; m >= 1; m /= 2) u += __shfl_xor_sync(0xffffffffu, u, m);
-    if (on && q == 0) {
-        if (known) {
-            if (p.skip) u = fmaf(p.skip[d], xv, u);
-            if (p.z) {
-                const float zv = to_f(static_cast<const T *>(p.z)[r * p.z_row + d]);
-                u *= zv * sigmoidf(zv);
-            }
+    for (int i = 0; i < kRows; ++i) h[i] = st[i] ? load_state(st[i]) : zero_state();
+    const f32x2 k = dup(kLog2e);
+    const State A = on ? load_state(p.A + (long long)d * kN + 4 * q) : zero_state(), A2 = State{mul2(A.a, k), mul2(A.b, k)};
+    const float bias = on && p.dt_bias ? p.dt_bias[d] : 0.f, skip = on && p.skip ? p.skip[d] : 0.f;
+    const int at = (on ? d / p.Dg : 0) * kN + 4 * q;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const long long r = r0 + i;
+        float u = 0.f, xv = 0.f;
+        if (st[i]) {
+            const State Bt = four(static_cast<const T *>(p.Bm) + r * p.b_row + at), Ct = four(static_cast<const T *>(p.Cm) + r * p.c_row + at);
+            xv = to_f(static_cast<const T *>(p.x)[r * p.x_row + d]);
+            const float raw = to_f(static_cast<const T *>(p.dt)[r * p.dt_row + d]) + bias;
+            const float s = p.softplus ? softplusf(raw) : raw;
+            h[i] = advance(decay(A2, dup(s)), h[i], dup(s * xv), Bt);
+            store_state(st[i], h[i]);
+            u = dot(h[i], Ct);
         }
-        from_f(static_cast<T *>(p.y)[(long long)r * p.D + d], u);
+#pragma unroll
+        for (int m = kL / 2; m >= 1; m /= 2) u += __shfl_xor_sync(0xffffffffu, u, m);
+        if (on && q == 0 && r < p.rows) {
+            if (st[i]) {
+                u = fmaf(skip, xv, u);
+                if (p.z) {
+                    const float zv = to_f(static_cast<const T *>(p.z)[r * p.z_row + d]);
+                    u *= zv * sigmoidf(zv);
+                }
+            }
+            from_f(static_cast<T *>(p.y)[r * p.D + d], u);
+        }
     }
 }
 
@@ -1150,11 +1253,16 @@ int gdr_ssm_step(const gdr_ssm_step_args *a, void *stream) {
         return rc;
     if (!any) return GDR_OK;
     StepP p{a->x, a->dt, a->z, a->Bm, a->Cm, a->A, a->skip, a->dt_bias, a->state, a->slots, a->y,
-            a->x_row, a->dt_row, a->z_row, a->b_row, a->c_row, a->n_slots, (int)a->D, (int)(a->D / a->G), a->softplus};
+            a->x_row, a->dt_row, a->z_row, a->b_row, a->c_row, a->n_slots, (int)a->D, (int)(a->D / a->G), a->softplus, (int)a->rows};
     ssm_by_type(a->dtype, a->N, true, [&](auto t, auto l, auto) {
         constexpr int L = decltype(l)::value;
-        const int ch = kThreads / L;
-        k_ssm_step<decltype(t), L><<<dim3((unsigned)((a->D + ch - 1) / ch), (unsigned)a->rows), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        const long long tiles = (a->D + kThreads / L - 1) / (kThreads / L);
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        // four rows a thread once that leaves every SM some warps
+        if (tiles * a->rows >= 32LL * layer_sms())
+            k_ssm_step<decltype(t), L, 4><<<dim3((unsigned)tiles, (unsigned)((a->rows + 3) / 4)), kThreads, 0, st>>>(p);
+        else
+            k_ssm_step<decltype(t), L, 1><<<dim3((unsigned)tiles, (unsigned)a->rows), kThreads, 0, st>>>(p);
     });
     return layer_launched("scan step");
 }
