@@ -406,6 +406,32 @@ def test_matmul_does_not_read_past_its_operands(gdr):
     assert torch.equal(gdr.block_matmul_fp8(big[:M], sa, wide[:N], sb), want)
 
 
+def test_gradients_against_differences(gdr):
+    """Along each gradient, with steps h of a hundredth of the parameter's norm and of half that: a central difference
+    D(h) is off by c h^2 + O(h^4) (c is large for A, whose gradient lies in the few slowly decaying states), so
+    (4 D(h / 2) - D(h)) / 3 is off by O(h^4); the forward's rounding (2^-17 against a change of the loss of about a
+    hundredth) gives 1e-3: 2e-2 holds both."""
+    v, dy, _ = scan_inputs((1, 100, 32, 1, 16, None, False, True, True, True, True), "f32")
+    v.pop("initial_state")
+    gen = gen_of(30)
+    v["w"], v["b"], v["n"] = 0.5 * rand(gen, 32, 4), rand(gen, 32), 1 + 0.1 * rand(gen, 32)
+
+    def loss(p):
+        x, _ = gdr.short_conv(p["x"], p["w"], p["b"])
+        y, _ = gdr.state_space_scan(x, *(p[k] for k in ("dt", "A", "B", "C", "D", "z", "dt_bias")))
+        y, r = gdr.residual_rms_norm(y, p["n"], p["x"])
+        return (y.double() * dy).sum() + (r.double() * dy).sum()
+
+    leaves = {k: t.detach().requires_grad_() for k, t in v.items()}
+    grads = dict(zip(leaves, torch.autograd.grad(loss(leaves), list(leaves.values()))))
+    for k, g in grads.items():
+        move = g * (0.01 * v[k].detach().norm() / g.norm())
+        with torch.no_grad():
+            d1, d2 = ((loss({**v, k: v[k] + f * move}) - loss({**v, k: v[k] - f * move})) / (2 * f) for f in (1.0, 0.5))
+        diff, want = (4 * d2 - d1) / 3, (g.double() * move).sum()
+        assert abs(diff - want) <= 2e-2 * abs(want), (k, float(diff), float(want))
+
+
 # ---- across operators --------------------------------------------------------
 
 
