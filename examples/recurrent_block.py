@@ -125,7 +125,7 @@ def main():
     loss, grads = block.train_step(*(torch.randn(2, 64, block.width, device="cuda", generator=gen).bfloat16() for _ in range(3)))
     print(f"training step: loss {float(loss):.4f}, gradient norms " + ", ".join(f"{k} {float(g.float().norm()):.2e}" for k, g in grads.items()))
 
-    heads, width = 8, block.width
+    heads, width = 4, block.width
     weight = quantise_weight(torch.randn(3 * heads * 128, width, device="cuda", generator=gen) * width ** -0.5)
     g = -torch.rand(128, heads, device="cuda", generator=gen)
     o, state = delta_prompt(h, weight, (g, torch.sigmoid(torch.randn(128, heads, device="cuda", generator=gen))),
