@@ -116,23 +116,16 @@ __device__ __forceinline__ void pack8(const float (&f)[8], Raw8<float> &r) {
         r.w[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
                             __float_as_uint(f[4 * i + 3]));
 }
-// Loads eight elements from p, of which the first n exist (zeros for the rest).
-// kVec: p is 16-byte aligned and n is 8 or not positive.
-template <typename T, bool kVec>
+// Loads eight elements from p (16-byte aligned), zeros if n is not positive.
+template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T *p, int n) {
     Raw8<T> r;
-    if (kVec) {
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-            r.w[i] = n > 0 ? reinterpret_cast<const uint4 *>(p)[i] : make_uint4(0, 0, 0, 0);
-    } else {
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < n ? to_f(p[i]) : 0.f;
-        pack8(f, r);
-    }
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+        r.w[i] = n > 0 ? reinterpret_cast<const uint4 *>(p)[i] : make_uint4(0, 0, 0, 0);
     return r;
 }
+// Stores the first n of eight elements (kVec: p is 16-byte aligned and n is 8 or not positive).
 template <typename T, bool kVec>
 __device__ __forceinline__ void store8(T *p, const float (&f)[8], int n) {
     if (kVec) {

@@ -44,8 +44,8 @@ struct Piece {
 // is the tensor's too.
 template <typename T, bool kShift>
 __device__ __forceinline__ Raw8<T> load_piece(const T *row, const Piece &k, bool vec, bool inner) {
-    if (!kShift) return load8<T, true>(row + k.c, k.hi);
-    if (vec && (k.whole() || inner)) return load8<T, true>(row + k.c, k.hi > 0 ? 8 : 0);
+    if (!kShift) return load8<T>(row + k.c, k.hi);
+    if (vec && (k.whole() || inner)) return load8<T>(row + k.c, k.hi > 0 ? 8 : 0);
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = e >= k.lo && e < k.hi ? to_f(row[k.c + e]) : 0.f;

@@ -154,7 +154,7 @@ struct Flight {
     int off, n;
     __device__ __forceinline__ void fetch(const T *p, int count) {  // count elements exist, at most eight
         if (kVec) {
-            const Raw8<T> r = load8<T, true>(p, count);
+            const Raw8<T> r = load8<T>(p, count);
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) w[i] = r.w[i];
             return;
