@@ -19,8 +19,13 @@
 
 namespace {
 
-constexpr int kMaxThreads = 544, kMaxIter = 4;  // 8 x 512 x 4 channels a row, and a piece more where shifted
-constexpr int kMaxD = 8 * 512 * 4;
+constexpr int kMaxThreads = 512, kMaxIter = 4;
+constexpr int kMaxD = 8 * kMaxThreads * kMaxIter;
+// A shifted row of more than kMaxD - 7 channels may lie in one piece more than
+// kMaxThreads x kMaxIter: it takes five pieces a thread (kIter = 5).
+constexpr int kWideThreads = 416;
+static_assert(8 * kWideThreads * (kMaxIter + 1) >= kMaxD + 7, "the widest row");
+constexpr int max_threads(int iter) { return iter > kMaxIter ? kWideThreads : kMaxThreads; }
 
 struct NormP {
     const void *x, *residual;
@@ -109,6 +114,7 @@ __device__ __forceinline__ void load_weight(const float *w, const Piece &k, int 
 
 // Sum of (up to two) values over the CTA; `buf` alternates between calls so
 // that one barrier a call is enough.
+static_assert(kMaxThreads <= 16 * 32, "cta_sum adds the sums of 16 warps");
 __device__ __forceinline__ float2 cta_sum(float a, float b, float2 *buf) {
 #pragma unroll
     for (int m = 16; m >= 1; m /= 2) {
@@ -161,7 +167,7 @@ struct Divisor {
 };
 
 template <typename T, int kIter, bool kShift, bool kQuant>
-__global__ void __launch_bounds__(kIter == 4 ? kMaxThreads : 512, kIter == 4 ? 1 : 3) k_norm_fwd(const NormP p) {
+__global__ void __launch_bounds__(max_threads(kIter), kIter >= 4 ? 1 : 3) k_norm_fwd(const NormP p) {
     __shared__ float2 buf[32];
     __shared__ unsigned tops[kShift && kQuant ? 128 : 1];  // greatest magnitudes of the row's blocks, as ordered bits
     const long long row = blockIdx.x, out = row * p.D;
@@ -283,7 +289,7 @@ struct NormBwdP {
 // A CTA takes every gridDim-th row and keeps its part of dweight in registers
 // (kShift: gridDim is a multiple of eight, so that its rows begin alike).
 template <typename T, int kIter, bool kShift>
-__global__ void __launch_bounds__(kIter == 4 ? kMaxThreads : 512) k_norm_bwd(const NormBwdP p) {
+__global__ void __launch_bounds__(max_threads(kIter)) k_norm_bwd(const NormBwdP p) {
     __shared__ float2 buf[2][32];
     const int shift = kShift ? (int)(((long long)blockIdx.x * p.D) & 7) : 0;
     auto piece = [&](int i) { return Piece((int)(threadIdx.x + i * blockDim.x) * 8 - shift, p.D); };
@@ -371,11 +377,9 @@ int norm_sizes(long long M, long long D, int dtype) {
 // are in flight together.
 void shape_of(long long D, bool shift, int *threads, int *iter) {
     const int vecs = (int)((D + (shift ? 14 : 7)) / 8);  // a shifted row may need a piece more
-    int t = std::min(512, std::max(32, ((vecs + 1) / 2 + 31) / 32 * 32));
-    *threads = t;
-    if (vecs > t * kMaxIter) t += 32;
-    const int need = (vecs + t - 1) / t;
-    *iter = need <= 1 ? 1 : need <= 2 ? 2 : 4;
+    const int t = std::min(kMaxThreads, std::max(32, ((vecs + 1) / 2 + 31) / 32 * 32)), need = (vecs + t - 1) / t;
+    *threads = need > kMaxIter ? kWideThreads : t;
+    *iter = need <= 1 ? 1 : need <= 2 ? 2 : need <= kMaxIter ? 4 : 5;
 }
 
 int bwd_ctas(long long M, long long D) {
@@ -391,6 +395,7 @@ void norm_by_type(int dtype, int iter, bool shift, F f) {
         auto v = [&](auto l) {
             if (shift) f(t, l, std::true_type{}); else f(t, l, std::false_type{});
         };
+        if (iter == 5) return f(t, std::integral_constant<int, 5>{}, std::true_type{});  // shifted rows only
         if (iter == 1) v(std::integral_constant<int, 1>{});
         else if (iter == 2) v(std::integral_constant<int, 2>{});
         else v(std::integral_constant<int, 4>{});
