@@ -12,10 +12,12 @@
 // Accesses are of eight elements.  Where a row's length is not a multiple of
 // eight, rows begin inside one; there (kShift) a thread's eight channels are
 // those of an aligned piece of memory.  A row's first and last piece then
-// reaches into its neighbours: it is read whole all the same and cut in
-// registers (element by element only at the end of the tensor), and written
-// element by element.
+// reaches into its neighbours: it is read whole all the same where it lies
+// inside the tensor and cut in registers (element by element in the first and
+// last rows of a tensor that begins or ends in it), and written element by
+// element.
 #include "gdr_layer.h"
+#include "gdr_piece.h"
 
 namespace {
 
@@ -45,12 +47,12 @@ struct Piece {
     __device__ __forceinline__ Piece(int c_, int D) : c(c_), lo(max(0, -c_)), hi(min(8, D - c_)) {}
     __device__ __forceinline__ bool whole() const { return lo == 0 && hi == 8; }
 };
-// vec: pieces are aligned; inner: what lies up to seven elements around the row
-// is the tensor's too.
+// A piece of the i-th of M rows from base, `stride` elements apart (vec: pieces are aligned).
 template <typename T, bool kShift>
-__device__ __forceinline__ Raw8<T> load_piece(const T *row, const Piece &k, bool vec, bool inner) {
+__device__ __forceinline__ Raw8<T> load_piece(const T *base, long long i, long long M, int D, long long stride, const Piece &k, bool vec) {
+    const T *row = base + i * stride;
     if (!kShift) return load8<T>(row + k.c, k.hi);
-    if (vec && (k.whole() || inner)) return load8<T>(row + k.c, k.hi > 0 ? 8 : 0);
+    if (vec && (k.whole() || (k.hi > 0 && gdr::piece_inside(i, k.c, M, D, stride)))) return load8<T>(row + k.c, 8);
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = e >= k.lo && e < k.hi ? to_f(row[k.c + e]) : 0.f;
@@ -172,8 +174,7 @@ __global__ void __launch_bounds__(max_threads(kIter), kIter >= 4 ? 1 : 3) k_norm
     __shared__ unsigned tops[kShift && kQuant ? 128 : 1];  // greatest magnitudes of the row's blocks, as ordered bits
     const long long row = blockIdx.x, out = row * p.D;
     const int shift = kShift ? (int)(out & 7) : 0;
-    const T *x = static_cast<const T *>(p.x) + row * p.x_row;
-    const T *res = p.residual ? static_cast<const T *>(p.residual) + row * p.r_row : nullptr;
+    const T *x = static_cast<const T *>(p.x), *res = static_cast<const T *>(p.residual);
     if (kShift && kQuant)
         for (int i = threadIdx.x; i < 128; i += blockDim.x) tops[i] = 0;
     auto piece = [&](int i) { return Piece((int)(threadIdx.x + i * blockDim.x) * 8 - shift, p.D); };
@@ -181,8 +182,8 @@ __global__ void __launch_bounds__(max_threads(kIter), kIter >= 4 ? 1 : 3) k_norm
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
         const Piece k = piece(i);
-        rx[i] = load_piece<T, kShift>(x, k, p.x_vec, row + 1 < p.M && p.x_row >= p.D);
-        if (res) rr[i] = load_piece<T, kShift>(res, k, p.r_vec, row + 1 < p.M && p.r_row >= p.D);
+        rx[i] = load_piece<T, kShift>(x, row, p.M, p.D, p.x_row, k, p.x_vec);
+        if (res) rr[i] = load_piece<T, kShift>(res, row, p.M, p.D, p.r_row, k, p.r_vec);
     }
     float v[kIter][8], sq = 0.f;
 #pragma unroll
@@ -305,10 +306,9 @@ __global__ void __launch_bounds__(max_threads(kIter)) k_norm_bwd(const NormBwdP 
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
             const Piece k = piece(i);
-            const bool inner = row + 1 < p.M;
-            rr[i] = load_piece<T, kShift>(static_cast<const T *>(p.r) + at, k, p.vec, inner);
-            rg[i] = load_piece<T, kShift>(static_cast<const T *>(p.dy) + at, k, p.vec, inner);
-            if (p.dsum) rs[i] = load_piece<T, kShift>(static_cast<const T *>(p.dsum) + at, k, p.vec, inner);
+            rr[i] = load_piece<T, kShift>(static_cast<const T *>(p.r), row, p.M, p.D, p.D, k, p.vec);
+            rg[i] = load_piece<T, kShift>(static_cast<const T *>(p.dy), row, p.M, p.D, p.D, k, p.vec);
+            if (p.dsum) rs[i] = load_piece<T, kShift>(static_cast<const T *>(p.dsum), row, p.M, p.D, p.D, k, p.vec);
         }
         float sq = 0.f, gr = 0.f;
 #pragma unroll
