@@ -190,7 +190,9 @@ __device__ __forceinline__ float4 remote_f32x4(uint32_t saddr, int rank) {
 // Scales of a block: X's rows, Y's rows (or the block of them) as far as they
 // are needed, zeros past the edges.  The ring is sixteen deep: when the operand
 // ring (at most six deep) lets block i in, block i - 6's MMAs are done, so (with
-// at most four accumulators) block i - 10 has been taken.
+// at most four accumulators) block i - 10 has been taken, and block i - 11's
+// scales have been read.  A stage of the operand ring is free once its MMAs are
+// done and the scales' warp has passed it, so neither ring overtakes the other.
 constexpr int kScaleSlots = 16, kScaleRow = 132;
 // Asynchronous copy of one float, zero if it does not exist.
 __device__ __forceinline__ void copy_f32(float *to, const float *from, bool real) {
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(Cfg<kTN, kPair>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(&full[i], 1);
-            bar_init(&empty[i], 1);
+            bar_init(&empty[i], 2);  // the MMAs, and warp 2
         }
         for (int i = 0; i < kBufs; ++i) {
             bar_init(&tfull[i], 1);
@@ -306,6 +308,9 @@ __global__ void __launch_bounds__(Cfg<kTN, kPair>::kThreads, 1)
             const float *wt = (kSwap ? p.sx : p.sy) + (there ? nb * p.nk + kb0 : 0);
             for (int kb = kb0; kb < kb1; ++kb, ++it, tok += p.M, wt += there) {
                 if (it >= kStages && !(ok = bar_wait(&empty[it % kStages], (it / kStages - 1) & 1, abort))) break;
+                // Nothing but this arrival keeps the stage from being emptied again before this warp has looked:
+                // block it's MMAs need the scales of block it - kBufs only, and a second turn would undo the parity.
+                if (lane == 0) bar_arrive(&empty[it % kStages]);
                 float *sc = scales[it % kScaleSlots];
 #pragma unroll
                 for (int i = 0; i < kEach; ++i)
