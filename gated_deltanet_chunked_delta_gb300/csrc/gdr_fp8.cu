@@ -584,18 +584,16 @@ int launch(const CUtensorMap &mx, const CUtensorMap &my, const Fp8P &p, cudaStre
     cfg.attrs = at;
     cfg.numAttrs = 1;
     long long ctas = (long long)layer_sms() * (kTN <= 64 ? 2 : 1);
-    if (kPair) {  // pairs that run at a time (asked once): one more would take the whole time again
-        static int pairs = 0;
-        if (!pairs) {
-            int n = 0;
+    if (kPair) {  // pairs that run at a time (asked once a device): one more would take the whole time again
+        static gdr::OncePerDevice pairs;
+        const int n = pairs.get(layer_device(), 1, [&] {
+            int most = 0;
             cfg.gridDim = dim3((unsigned)(ctas & ~1LL));
-            if (cudaOccupancyMaxActiveClusters(&n, k_fp8_matmul<kTN, kSwap, kPair>, &cfg) != cudaSuccess || n < 1) {
-                cudaGetLastError();
-                n = 1;
-            }
-            pairs = n;
-        }
-        ctas = std::min(ctas, 2LL * pairs);
+            if (cudaOccupancyMaxActiveClusters(&most, k_fp8_matmul<kTN, kSwap, kPair>, &cfg) == cudaSuccess) return most;
+            cudaGetLastError();
+            return 0;
+        });
+        ctas = std::min(ctas, 2LL * n);
     }
     cfg.gridDim = dim3((unsigned)(kPair ? std::min(tiles, ctas / 2) * 2 : p.split > 1 ? tiles * p.split : std::min(tiles, ctas)));
     e = cudaLaunchKernelEx(&cfg, k_fp8_matmul<kTN, kSwap, kPair>, mx, my, p);

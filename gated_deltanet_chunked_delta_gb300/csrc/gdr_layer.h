@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "gdr.h"
+#include "gdr_once.h"
 
 namespace gdr {
 int set_last_error(int code, const char *msg);  // gdr_api.cu
@@ -52,21 +53,24 @@ inline int layer_launched(const char *what) {
 
 inline bool multiple16(const void *p) { return !(reinterpret_cast<uintptr_t>(p) & 15u); }
 
+// The current device, -1 when there is none.
+inline int layer_device() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess) return dev;
+    cudaGetLastError();
+    return -1;
+}
+
 // SM count of the current device, asked once a device (152 when none answers).
 inline int layer_sms() {
-    static int known[64];
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    static gdr::OncePerDevice known;
+    const int dev = layer_device();
+    return known.get(dev, 152, [&] {
+        int sms = 0;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) return sms;
         cudaGetLastError();
-        return 152;
-    }
-    if (known[dev] > 0) return known[dev];
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
-        cudaGetLastError();
-        return 152;
-    }
-    known[dev] = sms;
-    return sms;
+        return 0;
+    });
 }
 
 // ---- device ----------------------------------------------------------------
