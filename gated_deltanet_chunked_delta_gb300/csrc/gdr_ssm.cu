@@ -117,16 +117,22 @@ __device__ __forceinline__ void pass_state(const SsmP &p, const Place<kL> &w, co
 }
 
 // Segment boundary state from the summaries of segments j0, j0 + step, ..
-// up to (not including) seg: v <- e^{A sum s_j} v + summary_j.
+// up to (not including) seg: v <- e^{A sum s_j} v + summary_j.  Nothing comes
+// before the first of them, in which the sequence starts (or, backwards, ends);
+// its sum of s is left out, for it holds other sequences' tokens too, and 0
+// times the infinity or NaN that they can make of it is not 0.
 template <int kL>
 __device__ __forceinline__ State chain(const SsmP &p, const Place<kL> &w, const State &A2, int b, int j0, int seg, int step) {
     State v = zero_state();
     if (!w.on) return v;
     for (int j = j0; j != seg; j += step) {
         const long long row = (long long)b * p.S + j;
-        const float sum = p.sum_s[row * p.D + w.d];
-        const State a = decay(A2, dup(sum));
         const State e = load_state(p.sum_h + w.at(row, p));
+        if (j == j0) {
+            v = e;
+            continue;
+        }
+        const State a = decay(A2, dup(p.sum_s[row * p.D + w.d]));
         v = State{fma2(a.a, v.a, e.a), fma2(a.b, v.b, e.b)};
     }
     return v;

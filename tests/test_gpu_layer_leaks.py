@@ -1,0 +1,65 @@
+"""What one packed sequence holds, NaN and infinities included, changes nothing of another: each test runs a call with
+and without the foreign values and wants the other sequence's results bit for bit."""
+import pytest
+import torch
+
+from test_gpu_layer import DT, bounds, gdr, gen_of, rand, scan_inputs  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+PER_TOKEN = ("x", "dt", "B", "C", "z")
+
+
+def run_scan(gdr, v, dy, dht, lengths, softplus):  # noqa: F811
+    leaves = {k: t.detach().clone().requires_grad_() for k, t in v.items() if t is not None}
+    y, ht = gdr.state_space_scan(**{**v, **leaves}, dt_softplus=softplus, output_final_state=True, cu_seqlens=bounds(lengths))
+    return y.detach(), ht.detach(), dict(zip(leaves, torch.autograd.grad([y, ht], list(leaves.values()), [dy, dht])))
+
+
+def same(a, b, what):
+    assert torch.isfinite(a.float()).all(), what
+    assert torch.equal(a, b), what
+
+
+def scan_case(gdr, lengths, D, G, N, dt, foul, softplus=True, bias=True):  # noqa: F811
+    """``foul`` changes the inputs of one of two sequences and says which."""
+    T = sum(lengths)
+    v, dy, dht = scan_inputs((1, T, D, G, N, lengths, True, True, True, bias, softplus), dt)
+    clean = run_scan(gdr, v, dy, dht, lengths, softplus)
+    w = {k: None if t is None else t.clone() for k, t in v.items()}
+    bad = foul(w)
+    fouled = run_scan(gdr, w, dy, dht, lengths, softplus)
+    assert not torch.isfinite(fouled[0]).all()  # it was foul indeed
+    keep = 1 - bad
+    at = slice(0, lengths[0]) if keep == 0 else slice(lengths[0], T)
+    same(fouled[0][:, at], clean[0][:, at], "y")
+    same(fouled[1][keep], clean[1][keep], "final")
+    for k in PER_TOKEN:
+        same(fouled[2][k][:, at], clean[2][k][:, at], k)
+    same(fouled[2]["initial_state"][keep], clean[2]["initial_state"][keep], "initial_state")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G,N", [(40, 1, 16), (33, 1, 8), (16, 2, 32)])
+@pytest.mark.parametrize("bad", [0, 1])
+def test_scan_nan_steps_stay_in_their_sequence(gdr, bad, D, G, N, dt):  # noqa: F811
+    """Long enough to be cut into segments, the sequences' border inside one of them."""
+    lengths = (1501, 1499)
+
+    def foul(v):
+        v["dt"][0, 1495 if bad == 0 else 1510, 5] = NAN
+        return bad
+    scan_case(gdr, lengths, D, G, N, dt, foul)
+
+
+@pytest.mark.parametrize("bad", [0, 1])
+def test_scan_overflowing_steps_stay_in_their_sequence(gdr, bad):  # noqa: F811
+    """Without the softplus, steps of one sequence that make every decay a growth (e^{A sum s} overflows).  No bias: it
+    would turn some of the other sequence's steps negative too."""
+    lengths = (1501, 1499)
+
+    def foul(v):
+        v["dt"][0, slice(0, 1501) if bad == 0 else slice(1501, 3000)] = -2.0
+        return bad
+    scan_case(gdr, lengths, 24, 1, 16, "f32", foul, softplus=False, bias=False)
