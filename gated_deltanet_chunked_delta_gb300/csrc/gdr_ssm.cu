@@ -808,11 +808,13 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) k_ssm_bw
         State A2r = A2;  // opaque, or the compiler keeps the forward's decays (and spills them)
         asm volatile("" : "+l"(A2r.a), "+l"(A2r.b));
         // Tokens lo .. hi - 1 of the tile, all of one sequence, from state h.
-        // kPart: the others change nothing (s = 0, du = 0) and leave no result.
+        // kPart: the others change nothing (s, du, B and C are taken as 0, not
+        // multiplied by it: they may be NaN or infinite) and leave no result.
         auto tile = [&](auto some, State h, int lo, int hi) {
             constexpr bool kPart = decltype(some)::value;
             const State hs = h;
             auto mine = [&](int r) { return !kPart || (r >= lo && r < hi); };
+            auto load = [&](const float(&from)[kBack][kN], int r) { return mine(r) ? load_state(&from[r][w.n0]) : zero_state(); };
             auto factors = [&](int r, f32x2 &s2, f32x2 &i2, f32x2 &d2) {
                 const float2 in = sm.in[buf][r][pair_place<kCh>(r, w.ch)];
                 const float du = sm.du[buf][r][w.ch];
@@ -831,9 +833,9 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) k_ssm_bw
                     const int r = g + k;
                     f32x2 s2, i2, d2;
                     factors(r, s2, i2, d2);
-                    h = advance(decay(A2, s2), h, i2, load_state(&sm.B[buf][r][w.n0]));
+                    h = advance(decay(A2, s2), h, i2, load(sm.B[buf], r));
                     H[r] = h;
-                    u[k] = dot(h, load_state(&sm.C[buf][r][w.n0]));
+                    u[k] = dot(h, load(sm.C[buf], r));
                     c[k] = fold_channels<kL>(State{mul2(d2, h.a), mul2(d2, h.b)});
                 }
 #pragma unroll
@@ -853,7 +855,7 @@ __global__ void __launch_bounds__(2 * kThreads, sizeof(T) == 2 ? 2 : 1) k_ssm_bw
                     const int r = g + k;
                     f32x2 s2, i2, d2;
                     factors(r, s2, i2, d2);
-                    const State C = load_state(&sm.C[buf][r][w.n0]), Bt = load_state(&sm.B[buf][r][w.n0]);
+                    const State C = load(sm.C[buf], r), Bt = load(sm.B[buf], r);
                     e = State{fma2(d2, C.a, e.a), fma2(d2, C.b, e.b)};
                     eb[k] = dot(e, Bt);
                     c[k] = fold_channels<kL>(State{mul2(i2, e.a), mul2(i2, e.b)});

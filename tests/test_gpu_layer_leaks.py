@@ -63,3 +63,17 @@ def test_scan_overflowing_steps_stay_in_their_sequence(gdr, bad):  # noqa: F811
         v["dt"][0, slice(0, 1501) if bad == 0 else slice(1501, 3000)] = -2.0
         return bad
     scan_case(gdr, lengths, 24, 1, 16, "f32", foul, softplus=False, bias=False)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [(30, 34), (1501, 1499)], ids=str)
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("bad", [0, 1])
+def test_scan_foul_tokens_beside_the_border(gdr, bad, value, lengths, dt):  # noqa: F811
+    """Inputs, gates, B and C of the tokens next to the border, in the tile that both sequences share."""
+    def foul(v):
+        at = slice(lengths[0] - 3, lengths[0]) if bad == 0 else slice(lengths[0], lengths[0] + 3)
+        for k in PER_TOKEN:
+            v[k][0, at] = value
+        return bad
+    scan_case(gdr, lengths, 40, 1, 16, dt, foul)
