@@ -305,14 +305,16 @@ __global__ void __launch_bounds__(kCols *kRunsB) k_conv_bwd(const ConvP p) {
 #pragma unroll
                     for (int e = 0; e < kE; ++e) dp[e] = 0.f;
                 }
-                const int old = t < p.T ? t - s0 : W;  // tokens of this one's sequence before it
+                const int old = t < p.T ? t - s0 : -1;  // tokens of this one's sequence before it
                 float o[kE];
 #pragma unroll
                 for (int j = 0; j < W; ++j) {  // to the token W - 1 - j before this one
                     const bool same = W - 1 - j <= old;
 #pragma unroll
                     for (int e = 0; e < kE; ++e) {
-                        const float v = fmaf(same ? w[j][e] : 0.f, dp[e], j < W - 1 ? wait[j < W - 1 ? j : 0][e] : 0.f);
+                        // chosen, not multiplied by zero: another sequence's dp may be NaN or infinite
+                        const float before = j < W - 1 ? wait[j < W - 1 ? j : 0][e] : 0.f;
+                        const float v = same ? fmaf(w[j][e], dp[e], before) : before;
                         if (j == 0) o[e] = v;
                         else wait[j - 1 < 0 ? 0 : j - 1][e] = v;
                     }

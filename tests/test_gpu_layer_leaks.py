@@ -77,3 +77,34 @@ def test_scan_foul_tokens_beside_the_border(gdr, bad, value, lengths, dt):  # no
             v[k][0, at] = value
         return bad
     scan_case(gdr, lengths, 40, 1, 16, dt, foul)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [(30, 34), (3, 2), (128, 129)], ids=str)
+@pytest.mark.parametrize("D,W", [(64, 4), (37, 3), (30, 2)])
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("bad", [0, 1])
+def test_conv_foul_tokens_beside_the_border(gdr, bad, value, silu, D, W, lengths, dt):  # noqa: F811
+    gen, T = gen_of(31), sum(lengths)
+    x, dy, w, b = rand(gen, 1, T, D, dt=DT[dt]), rand(gen, 1, T, D, dt=DT[dt]), rand(gen, D, W), rand(gen, D)
+    h0, dht = rand(gen, 2, W - 1, D, dt=DT[dt]), rand(gen, 2, W - 1, D, dt=DT[dt])
+
+    def run(x, dy):
+        x, h = x.clone().requires_grad_(), h0.clone().requires_grad_()
+        y, ht = gdr.short_conv(x, w, b, "silu" if silu else None, h, True, bounds(lengths))
+        return (y.detach(), ht.detach(), *torch.autograd.grad([y, ht], [x, h], [dy, dht]))
+
+    at = slice(lengths[0] - 2, lengths[0]) if bad == 0 else slice(lengths[0], lengths[0] + 2)
+    clean = run(x, dy)
+    for foul_dy in (False, True):
+        fx, fdy = x.clone(), dy.clone()
+        (fdy if foul_dy else fx)[0, at] = value
+        fouled = run(fx, fdy)
+        assert not torch.isfinite(fouled[2 if foul_dy else 0]).all()
+        keep = 1 - bad
+        kept = slice(0, lengths[0]) if keep == 0 else slice(lengths[0], T)
+        for i, what in ((0, "y"), (2, "dx")):
+            same(fouled[i][:, kept], clean[i][:, kept], what)
+        for i, what in ((1, "final"), (3, "dinit")):
+            same(fouled[i][keep], clean[i][keep], what)
