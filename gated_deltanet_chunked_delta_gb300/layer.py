@@ -25,6 +25,7 @@ import struct
 from ctypes import c_float, c_int, c_longlong, c_size_t, c_void_p
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import GDR_BF16, GDR_F32, GdrError, load
 
@@ -179,6 +180,14 @@ def _wants_grad(*ts):
     return False
 
 
+def _no_tangents(name, *ts):
+    """Forward-mode derivatives are refused rather than dropped: a call without ``requires_grad`` meets no autograd."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:  # inside a dual level (asked at every call, so cheaply)
+        for t in ts:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                _fail(1, f"{name} has no forward-mode derivative: detach its inputs or use reverse mode")
+
+
 def _grad(g, like):
     """An incoming gradient as the kernels read it."""
     if g is None or (g.dtype is like.dtype and g.is_contiguous()):
@@ -266,6 +275,7 @@ def short_conv(x, weight, bias=None, activation="silu", initial_state=None, outp
     before each sequence, oldest first (zeros when absent).  Returns (y [B, T, D], final_state [N, W - 1, D] or None);
     differentiable in x, weight, bias and initial_state."""
     silu = _activation(activation)
+    _no_tangents("short_conv", x, weight, bias, initial_state)
     if _wants_grad(x, weight, bias, initial_state):
         return _ShortConv.apply(x, weight, bias, silu, initial_state, bool(output_final_state), cu_seqlens)
     return _conv_fwd(x, weight, bias, silu, initial_state, output_final_state, cu_seqlens)
@@ -276,6 +286,7 @@ def short_conv_step(x, weight, state, bias=None, activation="silu", slots=None):
     int32 names each row's state (row r uses slot r when absent), a negative one an idle row whose y is zero.
     Returns y [rows, D].  No gradient."""
     silu = _activation(activation)
+    _no_tangents("short_conv_step", x, weight, state, bias)
     dev, code = _inputs("x", x)
     if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
         _fail(2, "x must be [rows, D], weight [D, W] and state [n_slots, W - 1, D]")
@@ -396,6 +407,7 @@ def state_space_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=T
     when absent); N in 8, 16, 32, 64.  Without z there is no gate, without D no skip.  Returns (y [B, T, D],
     final_state [n_seqs, D, N] fp32 or None); differentiable in every tensor but cu_seqlens."""
     softplus = 1 if dt_softplus else 0
+    _no_tangents("state_space_scan", x, dt, A, B, C, D, z, dt_bias, initial_state)
     if _wants_grad(x, dt, A, B, C, D, z, dt_bias, initial_state):
         return _StateSpaceScan.apply(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, bool(output_final_state),
                                      cu_seqlens)
@@ -405,6 +417,7 @@ def state_space_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=T
 def state_space_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus=True, slots=None):
     """One token of every row: x, dt, z [rows, D]; B, C [rows, G, N]; state [n_slots, D, N] fp32, updated in place;
     slots as in ``short_conv_step``.  Returns y [rows, D].  No gradient."""
+    _no_tangents("state_space_step", x, dt, A, B, C, state, D, z, dt_bias)
     dev, code, d, n, g = _ssm_check(x, dt, A, B, C, D, z, dt_bias, 1)
     rows, n_slots = x.shape[0], state.shape[0]
     _param("state", state, dev, (n_slots, d, n))
@@ -496,6 +509,7 @@ def residual_rms_norm(x, weight, residual=None, eps=1e-6):
 
     x, residual [..., D]; weight [D] fp32; D at most 16384.  Returns (y, r); r is x itself without a residual.
     Differentiable in x, weight and residual, through y and r."""
+    _no_tangents("residual_rms_norm", x, weight, residual)
     if _wants_grad(x, weight, residual):
         return _ResidualRmsNorm.apply(x, weight, residual, float(eps))
     y, _, r = _norm_fwd(x, weight, residual, eps, False)
@@ -506,6 +520,7 @@ def residual_rms_norm_fp8(x, weight, residual=None, eps=1e-6):
     """The same norm written in 8 bits: returns (q, scales, r) with q [..., D] float8_e4m3fn, scales
     [ceil(D / 128), M] fp32 (M rows) and y = q * scale of its row and block of 128 channels; a block's scale is
     max(max|y|, 1e-30) / 448.  What ``block_matmul_fp8`` reads.  No gradient."""
+    _no_tangents("residual_rms_norm_fp8", x, weight, residual)
     if _wants_grad(x, weight, residual):
         _fail(1, "residual_rms_norm_fp8 has no gradient: call it under torch.no_grad() or use residual_rms_norm")
     return _norm_fwd(x, weight, residual, eps, True)
@@ -519,6 +534,7 @@ def block_matmul_fp8(a, a_scales, b, b_scales, out_dtype=torch.bfloat16):
 
     a [M, K] and b [N, K] float8_e4m3fn, K a multiple of 16; a_scales [ceil(K / 128), M] and b_scales
     [ceil(N / 128), ceil(K / 128)] fp32; out_dtype bf16 or fp32.  Returns out [M, N].  No gradient."""
+    _no_tangents("block_matmul_fp8", a_scales, b_scales)
     f8, dev = torch.float8_e4m3fn, a.get_device()
     if dev < 0:
         _fail(1, "a must live on the GPU")
