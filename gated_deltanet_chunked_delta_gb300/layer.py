@@ -26,6 +26,7 @@ from ctypes import c_float, c_int, c_longlong, c_size_t, c_void_p
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from .binding import GDR_BF16, GDR_F32, GdrError, load
 
@@ -302,6 +303,7 @@ def short_conv_step(x, weight, state, bias=None, activation="silu", slots=None):
     _run(_calls().gdr_conv_step,
          _CONV_STEP.pack(x.data_ptr(), weight.data_ptr(), _ptr(bias), state.data_ptr(), _ptr(slots), rows, d, n, x.stride(0),
                          w, code, silu, y.data_ptr()), dev)
+    increment_version(state)  # as torch's own in-place operations: a backward that saved it raises
     return y
 
 
@@ -430,6 +432,7 @@ def state_space_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_sof
                         state.data_ptr(), _ptr(slots), rows, d, g, n_slots, x.stride(0), dt.stride(0),
                         0 if z is None else z.stride(0), B.stride(0), C.stride(0), n, code, 1 if dt_softplus else 0,
                         y.data_ptr()), dev)
+    increment_version(state)
     return y
 
 
