@@ -535,17 +535,18 @@ def residual_rms_norm_fp8(x, weight, residual=None, eps=1e-6):
 def block_matmul_fp8(a, a_scales, b, b_scales, out_dtype=torch.bfloat16):
     """out[m, n] = sum over blocks k of 128 of a_scales[k, m] b_scales[n // 128, k] (a_k[m] . b_k[n]), summed in fp32.
 
-    a [M, K] and b [N, K] float8_e4m3fn, K a multiple of 16; a_scales [ceil(K / 128), M] and b_scales
-    [ceil(N / 128), ceil(K / 128)] fp32; out_dtype bf16 or fp32.  Returns out [M, N].  No gradient."""
+    a [..., K] (M rows) and b [N, K] float8_e4m3fn, contiguous, N at least 1 and K a positive multiple of 16; a_scales
+    [ceil(K / 128), M] and b_scales [ceil(N / 128), ceil(K / 128)] fp32; out_dtype bf16 or fp32.  Returns out [..., N].
+    No gradient."""
     _no_tangents("block_matmul_fp8", a_scales, b_scales)
     f8, dev = torch.float8_e4m3fn, a.get_device()
     if dev < 0:
         _fail(1, "a must live on the GPU")
-    if a.dim() != 2 or b.dim() != 2:
-        _fail(2, f"a must be [M, K] and b [N, K] (got {tuple(a.shape)}, {tuple(b.shape)})")
-    (m, k), n = a.shape, b.shape[0]
-    blocks = -(-k // 128)
-    _param("a", a, dev, (m, k), f8)
+    if a.dim() < 1 or b.dim() != 2:
+        _fail(2, f"a must be [..., K] and b [N, K] (got {tuple(a.shape)}, {tuple(b.shape)})")
+    lead, k, n = a.shape[:-1], a.shape[-1], b.shape[0]
+    m, blocks = lead.numel(), -(-k // 128)
+    _param("a", a, dev, a.shape, f8)
     _param("b", b, dev, (n, k), f8)
     _param("a_scales", a_scales, dev, (blocks, m))
     _param("b_scales", b_scales, dev, (-(-n // 128), blocks))
@@ -554,7 +555,7 @@ def block_matmul_fp8(a, a_scales, b, b_scales, out_dtype=torch.bfloat16):
         _fail(3, f"out_dtype must be torch.bfloat16 or torch.float32 (got {out_dtype})")
     if _wants_grad(a_scales, b_scales):
         _fail(1, "block_matmul_fp8 has no gradient: call it under torch.no_grad()")
-    out = _empty((m, n), dtype=out_dtype, device=a.device)
+    out = _empty((*lead, n), dtype=out_dtype, device=a.device)
     _run(_calls().gdr_fp8_matmul,
          _FP8.pack(a.data_ptr(), b.data_ptr(), a_scales.data_ptr(), b_scales.data_ptr(), m, n, k, code, out.data_ptr()), dev)
     return out
