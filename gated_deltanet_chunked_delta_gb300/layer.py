@@ -386,6 +386,8 @@ class _StateSpaceScan(torch.autograd.Function):
         n_seqs = x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
         dy = torch.zeros(x.shape, dtype=x.dtype, device=where) if dy is None else _grad(dy, x)
         dht = _grad(dht, A)
+        if dht is not None and dht.data_ptr() % 16:  # states are read sixteen bytes at a time
+            dht = dht.clone()
         new = lambda like: None if like is None else _empty(like.shape, dtype=like.dtype, device=where)  # noqa: E731
         dx, ddt, dA, dB, dC, dD, dz, db, dh0 = (new(v) for v in (x, dt, A, B, C, D, z, dt_bias, initial_state))
         head = _ssm_head(x, dt, A, B, C, D, z, dt_bias, ctx.softplus, initial_state, cu_seqlens, n_seqs, _DTYPES[x.dtype])
