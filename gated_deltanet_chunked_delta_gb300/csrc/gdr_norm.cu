@@ -155,21 +155,18 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // the correction values on the border of two 8-bit ones can take the wrong
 // side; a division in its place takes 84 us for 16384 x 4096, this 74.
 struct Divisor {
-    f32x2 inv, neg;
-    __device__ __forceinline__ explicit Divisor(float scale) {
-        const float r = 1.f / scale;
-        inv = mk2(r, r);
-        const float d = r > 0.f ? -scale : 0.f;  // an infinite scale has no remainder: finite / inf is 0
-        neg = mk2(d, d);
-    }
-    __device__ __forceinline__ f32x2 of(f32x2 y) const {
-        const f32x2 q = mul2(y, inv);
-        return fma2(fma2(q, neg, y), inv, q);
+    float inv, neg;
+    __device__ __forceinline__ explicit Divisor(float scale) : inv(1.f / scale) {
+        neg = inv > 0.f ? -scale : 0.f;  // an infinite scale has no remainder: finite / inf is 0
     }
 };
+__device__ __forceinline__ void divide2(float &a, float &b, const Divisor &by_a, const Divisor &by_b) {
+    const f32x2 y = mk2(a, b), inv = mk2(by_a.inv, by_b.inv), q = mul2(y, inv);
+    un2(fma2(fma2(q, mk2(by_a.neg, by_b.neg), y), inv, q), a, b);
+}
 
 template <typename T, int kIter, bool kShift, bool kQuant>
-__global__ void __launch_bounds__(max_threads(kIter), kIter >= 4 ? 1 : 3) k_norm_fwd(const NormP p) {
+__global__ void __launch_bounds__(max_threads(kIter), kIter >= 4 ? 1 : kShift && kQuant ? 2 : 3) k_norm_fwd(const NormP p) {
     __shared__ float2 buf[32];
     __shared__ unsigned tops[kShift && kQuant ? 128 : 1];  // greatest magnitudes of the row's blocks, as ordered bits
     const long long row = blockIdx.x, out = row * p.D;
@@ -239,10 +236,10 @@ __global__ void __launch_bounds__(max_threads(kIter), kIter >= 4 ? 1 : 3) k_norm
             if (k.hi <= 0) continue;
             if (threadIdx.x % 16 == 0) p.scales[(long long)(k.c / 128) * p.M + row] = scale;
             const Divisor by(scale);
-            float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) un2(by.of(mk2(v[i][e], v[i][e + 1])), o[e], o[e + 1]);
-            *reinterpret_cast<uint2 *>(p.q + out + k.c) = make_uint2(e4m3x4(o[0], o[1], o[2], o[3]), e4m3x4(o[4], o[5], o[6], o[7]));
+            for (int e = 0; e < 8; e += 2) divide2(v[i][e], v[i][e + 1], by, by);
+            *reinterpret_cast<uint2 *>(p.q + out + k.c) =
+                make_uint2(e4m3x4(v[i][0], v[i][1], v[i][2], v[i][3]), e4m3x4(v[i][4], v[i][5], v[i][6], v[i][7]));
         }
     }
     if (!kShift || !kQuant) return;
@@ -255,17 +252,10 @@ __global__ void __launch_bounds__(max_threads(kIter), kIter >= 4 ? 1 : 3) k_norm
         if (k.hi <= 0) continue;
         const int b0 = max(k.c, 0) / 128, b1 = min(k.c + 7, p.D - 1) / 128;
         const Divisor by0(scale_of(b0)), by1(scale_of(b1));
-        float o[8];
+        const int cut = b1 * 128 - k.c;  // the first channel of the second block
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const f32x2 y = mk2(v[i][e], v[i][e + 1]);
-            float lo, hi, lo1, hi1;
-            un2(by0.of(y), lo, hi);
-            un2(by1.of(y), lo1, hi1);
-            o[e] = k.c + e >= b1 * 128 ? lo1 : lo;
-            o[e + 1] = k.c + e + 1 >= b1 * 128 ? hi1 : hi;
-        }
-        const uint32_t lo = e4m3x4(o[0], o[1], o[2], o[3]), hi = e4m3x4(o[4], o[5], o[6], o[7]);
+        for (int e = 0; e < 8; e += 2) divide2(v[i][e], v[i][e + 1], e >= cut ? by1 : by0, e + 1 >= cut ? by1 : by0);
+        const uint32_t lo = e4m3x4(v[i][0], v[i][1], v[i][2], v[i][3]), hi = e4m3x4(v[i][4], v[i][5], v[i][6], v[i][7]);
         if (k.whole() && p.o_vec) {
             *reinterpret_cast<uint2 *>(p.q + out + k.c) = make_uint2(lo, hi);
         } else {
