@@ -312,9 +312,8 @@ __global__ void __launch_bounds__(kCols *kRunsB) k_conv_bwd(const ConvP p) {
                     const bool same = W - 1 - j <= old;
 #pragma unroll
                     for (int e = 0; e < kE; ++e) {
-                        // chosen, not multiplied by zero: another sequence's dp may be NaN or infinite
-                        const float before = j < W - 1 ? wait[j < W - 1 ? j : 0][e] : 0.f;
-                        const float v = same ? fmaf(w[j][e], dp[e], before) : before;
+                        // not the weight: another sequence's dp may be NaN or infinite
+                        const float v = fmaf(w[j][e], same ? dp[e] : 0.f, j < W - 1 ? wait[j < W - 1 ? j : 0][e] : 0.f);
                         if (j == 0) o[e] = v;
                         else wait[j - 1 < 0 ? 0 : j - 1][e] = v;
                     }
