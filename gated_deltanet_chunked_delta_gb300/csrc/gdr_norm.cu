@@ -5,8 +5,10 @@
 //   dr = rstd (w dy - r rstd^2 mean(w dy r)) + dsum,  dw = sum over rows of dy r rstd
 //
 // Bound by memory: a row is read once into the registers of one CTA, reduced
-// once, and written once (16384 x 4096 in 8 bits: 72 us, 6.5 TB/s; gradient of
-// 8192 x 4096: 71 us, 5.7 TB/s).  The norm is taken of r as it is stored, so that
+// once, and written once (16384 x 4096 in 8 bits: 74 us, 6.4 TB/s).  The
+// gradient of 8192 x 4096 takes 70 us with its sums, 3.8 TB/s: a CTA reads a row
+// only after the row before it has been reduced and written, so that nothing is
+// on its way meanwhile.  The norm is taken of r as it is stored, so that
 // the gradient, which reads the stored r, is that of what was computed.
 //
 // Accesses are of eight elements.  Where a row's length is not a multiple of
@@ -153,7 +155,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // correction by its remainder, which is exact (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990).  Without
 // the correction values on the border of two 8-bit ones can take the wrong
-// side; a division in its place takes 84 us for 16384 x 4096, this 74.
+// side; a division in its place takes 84 us for 16384 x 4096, this 74.  (Shifted
+// rows keep two scales a thread: at three CTAs of 512 threads an SM, 40 registers,
+// that spills and costs 7 %.)
 struct Divisor {
     float inv, neg;
     __device__ __forceinline__ explicit Divisor(float scale) : inv(1.f / scale) {

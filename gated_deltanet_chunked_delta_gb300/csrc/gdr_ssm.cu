@@ -26,7 +26,7 @@
 // states from the forward's checkpoints, one before every 16th token.
 //
 // 8192 tokens x 4096 channels x 16 states, bf16: 230 us (first form, one role
-// a thread: 402); 2 x 2048 tokens forward 115 us, backward 484 (1180).  What
+// a thread: 402); 2 x 2048 tokens forward 113 us, backward 493 (1180).  What
 // bounds them is the shared-memory pipe (28 and about 140 cycles a token of a
 // CTA) and, with one CTA an SM, the roles' own latencies.
 #include "gdr_layer.h"
@@ -958,9 +958,10 @@ __device__ __forceinline__ State four(const T *p) {
     return State{mk2(to_f(p[0]), to_f(p[1])), mk2(to_f(p[2]), to_f(p[3]))};
 }
 
-// Bound by memory: the states of the rows are read and written once (128 x 4096
-// x 16: 25 us from HBM, 20 where the states lie in L2; two or four rows a lane
-// were no faster).
+// The states of the rows are read and written once: 71 MB for 128 rows x 4096 x
+// 16 in bf16, 20.6 us (20.5 to 20.6 in nine runs of 24) where the states come from
+// HBM, 18.5 where a cache of 34 MB stays in L2; 3.5 TB/s.  A CTA waits for its
+// row's slot, then for its states, and ends: latencies rather than bandwidth.
 template <typename T, int kL>
 __global__ void __launch_bounds__(kThreads) k_ssm_step(const StepP p) {
     constexpr int kCh = kThreads / kL, kN = 4 * kL;

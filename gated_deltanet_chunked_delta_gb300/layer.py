@@ -14,9 +14,10 @@ Activations are bf16 or fp32 ``[B, T, ...]`` (one token: ``[rows, ...]``) with
 a contiguous innermost part; the strides between tokens and batch rows are
 free, so that slices of a projection's output go in as they are.  Parameters
 and recurrent states are fp32 (the convolution's state holds inputs, in their
-type).  Packed sequences: ``cu_seqlens`` int32 on the GPU with ``B = 1``; its
+type); the scan's A and states begin on 16-byte boundaries.  Packed sequences: ``cu_seqlens`` int32 on the GPU with ``B = 1``; its
 values are checked on the device (``check_status``).  Work is enqueued on the
-current stream of the inputs' device; nothing synchronises.
+current stream of the inputs' device; nothing synchronises.  Reverse mode only:
+inputs with forward-mode tangents are refused.
 """
 from __future__ import annotations
 
@@ -409,7 +410,11 @@ def state_space_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=T
 
     x, dt, z [B, T, D]; B, C [B, T, G, N]; A [D, N], D and dt_bias [D] fp32; initial_state [n_seqs, D, N] fp32 (zeros
     when absent); N in 8, 16, 32, 64.  Without z there is no gate, without D no skip.  Returns (y [B, T, D],
-    final_state [n_seqs, D, N] fp32 or None); differentiable in every tensor but cu_seqlens."""
+    final_state [n_seqs, D, N] fp32 or None); differentiable in every tensor but cu_seqlens.
+
+    The backward's workspace, held for the call, is 8 N bytes a token for every 512 / N channels of a group (16 KiB a
+    token at D = 4096, N = 16, one group; 256 KiB at N = 64), and a forward that keeps a gradient's states D N / 4 bytes
+    a token."""
     softplus = 1 if dt_softplus else 0
     _no_tangents("state_space_scan", x, dt, A, B, C, D, z, dt_bias, initial_state)
     if _wants_grad(x, dt, A, B, C, D, z, dt_bias, initial_state):

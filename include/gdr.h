@@ -275,7 +275,8 @@ GDR_API int gdr_conv_step(const gdr_conv_step_args *args, void *stream);
  * g = d / (D / G), with s_t = softplus(dt_t + dt_bias) (or dt_t + dt_bias):
  *     h_t = e^{s_t A} h_{t-1} + s_t x_t B_t,   u_t = C_t . h_t + skip x_t,   y_t = u_t silu(z_t) (or u_t).
  * `states` (nullable) keeps h before every GDR_SSM_STRIDE-th token of every
- * batch row for the backward. */
+ * batch row for the backward.  A, h0, ht, states, dht and dh0 are 16-byte
+ * aligned. */
 #define GDR_SSM_STRIDE 16
 typedef struct {
     const void *x, *dt, *z;     /* [B, T, D]; z nullable */
@@ -296,7 +297,10 @@ typedef struct {
     void *dB, *dC;              /* [B, T, G, N] */
     float *dA, *dskip, *ddt_bias; /* dskip iff skip, ddt_bias iff dt_bias */
     float *dh0;                 /* nullable */
-    void *workspace;            /* gdr_ssm_*_workspace_size bytes, 16-byte aligned (may be null when 0) */
+    /* gdr_ssm_*_workspace_size bytes, 16-byte aligned (may be null when 0).  The backward's holds each channel
+     * tile's part of dB and dC, 8 N bytes a token for every 512 / N channels of a group: at D = 4096 and one group
+     * 16 KiB a token for N = 16, 256 KiB for N = 64. */
+    void *workspace;
     size_t workspace_bytes;
 } gdr_ssm_args;
 GDR_API size_t gdr_ssm_fwd_workspace_size(const gdr_ssm_args *args);
@@ -304,7 +308,8 @@ GDR_API int gdr_ssm_fwd(const gdr_ssm_args *args, void *stream);
 GDR_API size_t gdr_ssm_bwd_workspace_size(const gdr_ssm_args *args);
 GDR_API int gdr_ssm_bwd(const gdr_ssm_args *args, void *stream);
 
-/* One token for each of `rows` sequences; slots as in gdr_conv_step. */
+/* One token for each of `rows` sequences; slots as in gdr_conv_step.  A and
+ * state are 16-byte aligned. */
 typedef struct {
     const void *x, *dt, *z;     /* [rows, D]; z nullable */
     const void *Bm, *Cm;        /* [rows, G, N] */
@@ -356,7 +361,7 @@ GDR_API int gdr_norm_bwd(const gdr_norm_bwd_args *args, void *stream);
 
 /* out[m, n] = sum_kb a_scales[kb, m] b_scales[n / 128, kb] sum_{k in block kb} a[m, k] b[n, k]:
  * e4m3 operands, blocks of 128 along k (the last may be short), sums in fp32.
- * K a multiple of 16; a, b 16-byte aligned. */
+ * N at least 1, K a positive multiple of 16; a, b and out 16-byte aligned. */
 typedef struct {
     const void *a, *b;          /* [M, K], [N, K] e4m3 */
     const float *a_scales, *b_scales; /* [ceil(K / 128), M], [ceil(N / 128), ceil(K / 128)] */
