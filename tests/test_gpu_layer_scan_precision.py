@@ -41,3 +41,20 @@ def test_errors_are_those_of_32_bits(gdr, ops, case, seed):  # noqa: F811
         found[name] = float((g.detach().double() - e).norm() / size), float((p.detach().double() - e).norm() / size)
     print({k: "%.2e against %.2e" % v for k, v in found.items()})
     assert all(mine <= max(1.5 * theirs, 2.0 ** -22) for mine, theirs in found.values()), found
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_tokens_without_a_step_change_nothing(gdr, dt):  # noqa: F811
+    """s = 0 is a decay of exactly 1, whatever A: states come out, and gradients go back, bit for bit."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    T, D, N = 333, 40, 16
+    x, BC = (torch.randn(2, T, D, device="cuda", generator=gen).to(dt), torch.randn(2, T, 1, N, device="cuda", generator=gen).to(dt))
+    A = -torch.logspace(-6, 6, D * N, device="cuda").view(D, N)
+    A[0] = 0
+    h0 = torch.randn(2, D, N, device="cuda", generator=gen).requires_grad_()
+    _, ht = gdr.state_space_scan(x, torch.zeros_like(x), A, BC, BC, dt_softplus=False, initial_state=h0, output_final_state=True)
+    dht = torch.randn(2, D, N, device="cuda", generator=gen)
+    assert torch.equal(ht, h0) and torch.equal(torch.autograd.grad(ht, h0, dht)[0], dht)
+    state = h0.detach().clone()
+    gdr.state_space_step(x[:, 0], torch.zeros_like(x[:, 0]), A, BC[:, 0], BC[:, 0], state, dt_softplus=False)
+    assert torch.equal(state, h0)
