@@ -72,11 +72,12 @@ __device__ __forceinline__ float dot(const State &x, const State &y) {
     un2(fma2(x.a, y.a, mul2(x.b, y.b)), lo, hi);
     return lo + hi;
 }
-// e^{s A} of four states, A2 = A log2 e.  For arguments between -1/4 and -2^-8
-// ex2.approx lies low by 2.0e-8 on average (measured: 7e-9 nearer to zero, single
-// values within 1.2e-7), and a slow state multiplies hundreds of decays: its
-// argument is moved up by as much, in the same instruction.  The move vanishes in
-// ex2.approx(0 + 2.2e-8) = 1 (measured), so that tokens without a step change nothing.
+// e^{s A} of four states, A2 = A log2 e.  ex2.approx lies low by 1.8e-8 to 2.7e-8
+// on average for arguments between -1/4 and -2^-8, by 5e-9 to 8e-9 nearer to zero
+// (measured; single values within 1.2e-7), and a slow state multiplies hundreds of
+// decays: the argument is moved up by what makes 1.5e-8 of the result, in the same
+// instruction.  ex2.approx(2.2e-8) is 1 (measured), so that tokens without a step
+// change nothing.
 __device__ __forceinline__ State decay(const State &A2, f32x2 s2) {
     const f32x2 low = dup(2.2e-8f);  // 1.5e-8 log2 e
     float a, b, c, d;

@@ -14,10 +14,11 @@ Activations are bf16 or fp32 ``[B, T, ...]`` (one token: ``[rows, ...]``) with
 a contiguous innermost part; the strides between tokens and batch rows are
 free, so that slices of a projection's output go in as they are.  Parameters
 and recurrent states are fp32 (the convolution's state holds inputs, in their
-type); the scan's A and states begin on 16-byte boundaries.  Packed sequences: ``cu_seqlens`` int32 on the GPU with ``B = 1``; its
-values are checked on the device (``check_status``).  Work is enqueued on the
-current stream of the inputs' device; nothing synchronises.  Reverse mode only:
-inputs with forward-mode tangents are refused.
+type); the scan's A and states begin on 16-byte boundaries.  Packed sequences:
+``cu_seqlens`` int32 on the GPU with ``B = 1``; its values are checked on the
+device (``check_status``).  Work is enqueued on the current stream of the
+inputs' device; nothing synchronises.  Reverse mode only: inputs with
+forward-mode tangents are refused.
 """
 from __future__ import annotations
 
