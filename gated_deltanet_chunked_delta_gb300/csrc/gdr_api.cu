@@ -32,6 +32,8 @@ unsigned tc_take_status(cudaStream_t st);
 unsigned conv_take_status(cudaStream_t st);
 unsigned ssm_take_status(cudaStream_t st);
 unsigned fp8_take_status(cudaStream_t st);
+unsigned linear_take_status(cudaStream_t st);
+unsigned delta_take_status(cudaStream_t st);
 }  // namespace gdr
 
 namespace {
@@ -474,7 +476,7 @@ int gdr_check_status(void *stream) {
     if (cudaStreamSynchronize(st) != cudaSuccess)
         return fail(GDR_ERR_CUDA, "stream error: %s", cudaGetErrorString(cudaGetLastError()));
     const unsigned s = simt_take_status(st) | tc_take_status(st) | conv_take_status(st) | ssm_take_status(st) |
-                       fp8_take_status(st);
+                       fp8_take_status(st) | linear_take_status(st) | delta_take_status(st);
     if (s & 0x80000000u) return fail(GDR_ERR_CUDA, "could not read the device status word");
     if (s & 1u) return fail(GDR_ERR_TIMEOUT, "a device-side wait ran out of polls");
     if (s & 2u) return fail(GDR_ERR_DEVICE, "a device-side index check failed");

@@ -1,5 +1,6 @@
 // gdr_layer.h -- shared by the layer operators around a recurrent mixer
-// (gdr_conv.cu, gdr_ssm.cu, gdr_norm.cu, gdr_fp8.cu): element access, the
+// (gdr_conv.cu, gdr_ssm.cu, gdr_linear.cu, gdr_delta.cu, gdr_norm.cu,
+// gdr_block.cu, gdr_fp8.cu): element access, the
 // scalar functions, sequence lookup and argument checks.  Not part of the ABI.
 #pragma once
 
@@ -20,6 +21,8 @@ int set_last_error(int code, const char *msg);  // gdr_api.cu
 unsigned conv_take_status(cudaStream_t st);
 unsigned ssm_take_status(cudaStream_t st);
 unsigned fp8_take_status(cudaStream_t st);
+unsigned linear_take_status(cudaStream_t st);
+unsigned delta_take_status(cudaStream_t st);
 }  // namespace gdr
 
 namespace {

@@ -5,8 +5,14 @@ CUDA kernels.
 * ``short_conv`` / ``short_conv_step``: depthwise causal convolution along the
   tokens (2 to 4 taps), over sequences and for one token of each;
 * ``state_space_scan`` / ``state_space_step``: the selective state space scan;
+* ``gated_linear_scan`` / ``gated_linear_step``: the gated linear recurrence of
+  one state a channel;
+* ``gated_delta_step``: one token through the gated delta rule, from the states
+  that ``chunk_gated_delta_rule`` returns;
 * ``residual_rms_norm`` / ``residual_rms_norm_fp8``: root-mean-square norm of a
   residual stream, in the input's type or in 8 bits with scales;
+* ``gated_residual_rms_norm``: the norm after a block with its gate, the residual
+  stream and the norm before the next block;
 * ``block_matmul_fp8``: product of 8-bit operands with a scale for each block
   of 128.
 
@@ -32,10 +38,12 @@ from torch.autograd.graph import increment_version
 
 from .binding import GDR_BF16, GDR_F32, GdrError, load
 
-__all__ = ["short_conv", "short_conv_step", "state_space_scan", "state_space_step", "residual_rms_norm",
-           "residual_rms_norm_fp8", "block_matmul_fp8"]
+__all__ = ["short_conv", "short_conv_step", "state_space_scan", "state_space_step", "gated_linear_scan",
+           "gated_linear_step", "gated_delta_step", "residual_rms_norm", "residual_rms_norm_fp8",
+           "gated_residual_rms_norm", "block_matmul_fp8"]
 
 STATE_STRIDE = 16  # GDR_SSM_STRIDE: tokens between the states kept for the backward
+LINEAR_STRIDE = 64  # GDR_LINEAR_STRIDE
 STATE_SIZES = (8, 16, 32, 64)
 
 _DTYPES = {torch.bfloat16: GDR_BF16, torch.float32: GDR_F32}
@@ -71,9 +79,24 @@ _NORM = _Args("gdr_norm_args", [("p", "x residual weight"), ("l", "M D x_row r_r
                                 ("p", "sum y q scales")])
 _NORM_BWD = _Args("gdr_norm_bwd_args", [("p", "r dy dsum weight"), ("l", "M D"), ("f", "eps"), ("i", "dtype"),
                                         ("p", "dr dweight workspace"), ("z", "workspace_bytes")])
+_LINEAR = _Args("gdr_linear_args", [
+    ("p", "x input_gate decay_gate z decay h0 cu_seqlens"), ("l", "B T D n_seqs"),
+    ("l", "x_row x_batch i_row i_batch r_row r_batch z_row z_batch"), ("f", "decay_scale"), ("i", "dtype"),
+    ("p", "y ht states dy dht dx di dr dz ddecay dh0 workspace"), ("z", "workspace_bytes")])
+_LINEAR_STEP = _Args("gdr_linear_step_args", [
+    ("p", "x input_gate decay_gate z decay state slots"), ("l", "rows D n_slots x_row i_row r_row z_row"),
+    ("f", "decay_scale"), ("i", "dtype"), ("p", "y")])
+_DELTA_STEP = _Args("gdr_delta_step_args", [
+    ("p", "q k v g beta state slots"), ("l", "rows Hq Hv n_slots q_row k_row v_row"), ("i", "K V"), ("f", "scale"),
+    ("i", "dtype"), ("p", "o")])
+_BLOCK_NORM = _Args("gdr_block_norm_args", [
+    ("p", "x gate residual weight next_weight"), ("l", "M D x_row gate_row residual_row"), ("f", "scale eps"), ("i", "dtype"),
+    ("p", "r y stats dr dy dx dgate dresidual dweight dnext_weight workspace"), ("z", "workspace_bytes")])
 _FP8 = _Args("gdr_fp8_args", [("p", "a b a_scales b_scales"), ("l", "M N K"), ("i", "out_dtype"), ("p", "out")])
 _ConvArgs, _ConvStepArgs, _SsmArgs, _SsmStepArgs, _NormArgs, _NormBwdArgs, _Fp8Args = (
     v.struct for v in (_CONV, _CONV_STEP, _SSM, _SSM_STEP, _NORM, _NORM_BWD, _FP8))
+_LinearArgs, _LinearStepArgs, _DeltaStepArgs, _BlockNormArgs = (
+    v.struct for v in (_LINEAR, _LINEAR_STEP, _DELTA_STEP, _BLOCK_NORM))
 
 _lib = None
 
@@ -83,11 +106,13 @@ def _calls():
     if _lib is None:
         lib = load()
         for name in ("conv_fwd", "conv_bwd", "conv_step", "ssm_fwd", "ssm_bwd", "ssm_step", "norm_fwd", "norm_bwd",
-                     "fp8_matmul"):
+                     "fp8_matmul", "linear_fwd", "linear_bwd", "linear_step", "delta_step", "block_norm_fwd",
+                     "block_norm_bwd"):
             f = getattr(lib, "gdr_" + name)
             f.argtypes, f.restype = [c_void_p, c_void_p], c_int
         for name, kinds in (("conv_bwd", [c_longlong] * 3 + [c_int]), ("ssm_fwd", [c_void_p]), ("ssm_bwd", [c_void_p]),
-                            ("norm_bwd", [c_longlong] * 2)):
+                            ("norm_bwd", [c_longlong] * 2), ("linear_fwd", [c_longlong] * 3),
+                            ("linear_bwd", [c_longlong] * 3), ("block_norm_bwd", [c_longlong] * 2)):
             f = getattr(lib, f"gdr_{name}_workspace_size")
             f.argtypes, f.restype = kinds, c_size_t
         _lib = lib
@@ -444,6 +469,168 @@ def state_space_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_sof
     return y
 
 
+# ---- gated linear recurrence ------------------------------------------------
+
+
+def _linear_check(x, input_gate, decay_gate, decay, z, decay_scale, lead):
+    """Shapes of the scan (lead 2: [B, T, D]) and of its step (lead 1: [rows, D])."""
+    dev, code = _inputs("x", x)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != lead + 1:
+        _fail(2, f"x must be {'[B, T, D]' if lead == 2 else '[rows, D]'} (got {tuple(shape)})")
+    _like("input_gate", input_gate, dev, dtype, shape)
+    _like("decay_gate", decay_gate, dev, dtype, shape)
+    if z is not None:
+        _like("z", z, dev, dtype, shape)
+    _param("decay", decay, dev, (shape[-1],))
+    if not 0.0 < decay_scale < 3e38:
+        _fail(1, f"decay_scale must be positive and finite (got {decay_scale})")
+    return dev, code
+
+
+def _linear_head(x, input_gate, decay_gate, decay, z, decay_scale, initial_state, cu_seqlens, n_seqs):
+    """The first 21 fields of the scan's arguments: inputs, sizes, strides, kinds."""
+    b, t, d = x.shape
+    xs, gs, rs = x.stride(), input_gate.stride(), decay_gate.stride()
+    zs = (0, 0) if z is None else z.stride()
+    return (x.data_ptr(), input_gate.data_ptr(), decay_gate.data_ptr(), _ptr(z), decay.data_ptr(), _ptr(initial_state),
+            _ptr(cu_seqlens), b, t, d, n_seqs, xs[1], xs[0], gs[1], gs[0], rs[1], rs[0], zs[1], zs[0], decay_scale,
+            _DTYPES[x.dtype])
+
+
+def _linear_fwd(x, input_gate, decay_gate, decay, z, decay_scale, initial_state, output_final_state, cu_seqlens, keep):
+    dev, _ = _linear_check(x, input_gate, decay_gate, decay, z, decay_scale, 2)
+    n_seqs = _sequences(x, dev, cu_seqlens)
+    (b, t, d), where = x.shape, x.device
+    if initial_state is not None:
+        _param("initial_state", initial_state, dev, (n_seqs, d))
+    y = _empty((b, t, d), dtype=x.dtype, device=where)
+    ht = _empty((n_seqs, d), dtype=_F32, device=where) if output_final_state else None
+    states = _empty((b, -(-t // LINEAR_STRIDE), d), dtype=_F32, device=where) if keep else None
+    lib = _calls()
+    size = lib.gdr_linear_fwd_workspace_size(b, t, d)
+    ws = _empty(size, dtype=torch.uint8, device=where) if size else None
+    _run(lib.gdr_linear_fwd,
+         _LINEAR.pack(*_linear_head(x, input_gate, decay_gate, decay, z, decay_scale, initial_state, cu_seqlens, n_seqs),
+                      y.data_ptr(), _ptr(ht), _ptr(states), 0, 0, 0, 0, 0, 0, 0, 0, _ptr(ws), size), dev)
+    return y, ht, states
+
+
+class _GatedLinearScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, input_gate, decay_gate, decay, z, decay_scale, initial_state, output_final_state, cu_seqlens):
+        ctx.set_materialize_grads(False)
+        y, ht, states = _linear_fwd(x, input_gate, decay_gate, decay, z, decay_scale, initial_state, output_final_state,
+                                    cu_seqlens, True)
+        ctx.save_for_backward(x, input_gate, decay_gate, decay, z, initial_state, cu_seqlens, states)
+        ctx.decay_scale = decay_scale
+        return y, ht
+
+    @staticmethod
+    def backward(ctx, dy, dht):
+        _once()
+        x, input_gate, decay_gate, decay, z, initial_state, cu_seqlens, states = ctx.saved_tensors
+        (b, t, d), where = x.shape, x.device
+        n_seqs = b if cu_seqlens is None else cu_seqlens.shape[0] - 1
+        dy = torch.zeros((b, t, d), dtype=x.dtype, device=where) if dy is None else _grad(dy, x)
+        dht = _grad(dht, decay)
+        new = lambda like: None if like is None else _empty(like.shape, dtype=like.dtype, device=where)  # noqa: E731
+        dx, di, dr, dz, ddecay, dh0 = (new(v) for v in (x, input_gate, decay_gate, z, decay, initial_state))
+        lib = _calls()
+        size = lib.gdr_linear_bwd_workspace_size(b, t, d)
+        ws = _empty(size, dtype=torch.uint8, device=where) if size else None
+        _run(lib.gdr_linear_bwd,
+             _LINEAR.pack(*_linear_head(x, input_gate, decay_gate, decay, z, ctx.decay_scale, initial_state, cu_seqlens, n_seqs),
+                          0, 0, states.data_ptr(), dy.data_ptr(), _ptr(dht), dx.data_ptr(), di.data_ptr(), dr.data_ptr(),
+                          _ptr(dz), ddecay.data_ptr(), _ptr(dh0), _ptr(ws), size), x.get_device())
+        return dx, di, dr, ddecay, dz, None, dh0, None, None
+
+
+def gated_linear_scan(x, input_gate, decay_gate, decay, z=None, decay_scale=8.0, initial_state=None, output_final_state=False,
+                      cu_seqlens=None):
+    """For every sequence and channel, with a_t = exp(-decay_scale softplus(decay) sigmoid(decay_gate_t)):
+
+        h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t,    y_t = h_t silu(z_t)
+
+    (y_t = h_t without z).  x, input_gate, decay_gate, z [B, T, D]; decay [D] fp32; initial_state [n_seqs, D] fp32 (zeros
+    when absent).  Returns (y [B, T, D], final_state [n_seqs, D] fp32 or None); differentiable in every tensor but
+    cu_seqlens.
+
+    The workspace, held for the call, is 16 bytes a channel for every 128 tokens (64 and 4 bytes more in the backward);
+    a forward that keeps a gradient holds states of 4 bytes a channel for every 64 tokens."""
+    _no_tangents("gated_linear_scan", x, input_gate, decay_gate, decay, z, initial_state)
+    decay_scale = float(decay_scale)
+    if _wants_grad(x, input_gate, decay_gate, decay, z, initial_state):
+        return _GatedLinearScan.apply(x, input_gate, decay_gate, decay, z, decay_scale, initial_state, bool(output_final_state),
+                                      cu_seqlens)
+    return _linear_fwd(x, input_gate, decay_gate, decay, z, decay_scale, initial_state, output_final_state, cu_seqlens, False)[:2]
+
+
+def gated_linear_step(x, input_gate, decay_gate, decay, state, z=None, decay_scale=8.0, slots=None):
+    """One token of every row: x, input_gate, decay_gate, z [rows, D]; state [n_slots, D] fp32, updated in place; slots as
+    in ``short_conv_step``.  Returns y [rows, D].  No gradient."""
+    _no_tangents("gated_linear_step", x, input_gate, decay_gate, decay, state, z)
+    dev, code = _linear_check(x, input_gate, decay_gate, decay, z, decay_scale, 1)
+    (rows, d), n_slots = x.shape, state.shape[0] if state.dim() else 0
+    _param("state", state, dev, (n_slots, d))
+    _slots(slots, dev, rows, n_slots)
+    if _wants_grad(x, input_gate, decay_gate, decay, z, state):
+        _fail(1, "gated_linear_step has no gradient: call it under torch.no_grad() or detach its inputs")
+    y = _empty((rows, d), dtype=x.dtype, device=x.device)
+    _run(_calls().gdr_linear_step,
+         _LINEAR_STEP.pack(x.data_ptr(), input_gate.data_ptr(), decay_gate.data_ptr(), _ptr(z), decay.data_ptr(), state.data_ptr(),
+                           _ptr(slots), rows, d, n_slots, x.stride(0), input_gate.stride(0), decay_gate.stride(0),
+                           0 if z is None else z.stride(0), decay_scale, code, y.data_ptr()), dev)
+    increment_version(state)
+    return y
+
+
+# ---- one token through the gated delta rule ----------------------------------
+
+
+def _heads(name, t):
+    if t.dim() != 3:
+        _fail(2, f"{name} must be [rows, heads, channels] (got {tuple(t.shape)})")
+    if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
+        _fail(1, f"{name} must be contiguous over its last two dimensions")
+
+
+def gated_delta_step(q, k, v, g, beta, state, scale=None, slots=None):
+    """One token of every row through the recurrence of ``chunk_gated_delta_rule``, S the state of the row's slot:
+
+        S <- e^g S,    w = beta (v - S^T k),    S <- S + k w^T,    o = scale S^T q.
+
+    q, k [rows, H_q, K]; v [rows, H_v, V] (H_v a multiple of H_q; K in 64, 128, 192; V in 64, 128, 192, 256); g (the
+    log-decay) and beta (after its sigmoid) [rows, H_v] fp32; state [n_slots, H_v, K, V] fp32, beginning on a 16-byte
+    boundary, updated in place (the final_state of a prompt goes in as it is); scale K^-1/2 when absent; slots as in
+    ``short_conv_step``.  Returns o [rows, H_v, V] in q's dtype.  No gradient."""
+    _no_tangents("gated_delta_step", q, k, v, g, beta, state)
+    dev, code = _inputs("q", q)
+    _heads("q", q)
+    rows, hq, kd = q.shape
+    _like("k", k, dev, q.dtype, q.shape)
+    _heads("k", k)
+    _heads("v", v)
+    hv, vd = v.shape[1:]
+    _like("v", v, dev, q.dtype, (rows, hv, vd))
+    _param("g", g, dev, (rows, hv))
+    _param("beta", beta, dev, (rows, hv))
+    if state.dim() != 4:
+        _fail(2, f"state must be [n_slots, H_v, K, V] (got {tuple(state.shape)})")
+    n_slots = state.shape[0]
+    _param("state", state, dev, (n_slots, hv, kd, vd))
+    _slots(slots, dev, rows, n_slots)
+    if _wants_grad(q, k, v, g, beta, state):
+        _fail(1, "gated_delta_step has no gradient: call it under torch.no_grad() or detach its inputs")
+    o = _empty((rows, hv, vd), dtype=q.dtype, device=q.device)
+    _run(_calls().gdr_delta_step,
+         _DELTA_STEP.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _ptr(slots),
+                          rows, hq, hv, n_slots, q.stride(0), k.stride(0), v.stride(0), kd, vd,
+                          kd ** -0.5 if scale is None else scale, code, o.data_ptr()), dev)
+    increment_version(state)
+    return o
+
+
 # ---- norm of the residual stream --------------------------------------------
 
 
@@ -535,6 +722,86 @@ def residual_rms_norm_fp8(x, weight, residual=None, eps=1e-6):
     if _wants_grad(x, weight, residual):
         _fail(1, "residual_rms_norm_fp8 has no gradient: call it under torch.no_grad() or use residual_rms_norm")
     return _norm_fwd(x, weight, residual, eps, True)
+
+
+# ---- norm after a block --------------------------------------------------------
+
+
+def _block_head(x, weight, gate, residual, next_weight, scale, eps):
+    """The first 13 fields of the block norm's arguments."""
+    d = x.shape[-1]
+    x2 = _rows("x", x, d)
+    g2, r2 = (None if t is None else _rows(n, t, d) for n, t in (("gate", gate), ("residual", residual)))
+    return (x2.data_ptr(), _ptr(g2), _ptr(r2), weight.data_ptr(), _ptr(next_weight), x2.shape[0], d, x2.stride(0),
+            0 if g2 is None else g2.stride(0), 0 if r2 is None else r2.stride(0), scale, eps, _DTYPES[x.dtype])
+
+
+def _block_fwd(x, weight, gate, residual, next_weight, scale, eps, keep):
+    dev, _ = _inputs("x", x)
+    shape, where = x.shape, x.device
+    if not shape or shape[-1] < 1:
+        _fail(2, f"x must be [..., D] (got {tuple(shape)})")
+    d = shape[-1]
+    _param("weight", weight, dev, (d,))
+    if gate is not None:
+        _like("gate", gate, dev, x.dtype, shape)
+    if residual is not None:
+        _like("residual", residual, dev, x.dtype, shape)
+    if next_weight is not None:
+        _param("next_weight", next_weight, dev, (d,))
+    head = _block_head(x, weight, gate, residual, next_weight, scale, eps)
+    r = _empty(shape, dtype=x.dtype, device=where)
+    y = None if next_weight is None else _empty(shape, dtype=x.dtype, device=where)
+    stats = _empty((head[5], 2), dtype=_F32, device=where) if keep else None
+    _run(_calls().gdr_block_norm_fwd,
+         _BLOCK_NORM.pack(*head, r.data_ptr(), _ptr(y), _ptr(stats), 0, 0, 0, 0, 0, 0, 0, 0, 0), dev)
+    return y, r, stats
+
+
+class _GatedResidualRmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, gate, residual, next_weight, scale, eps):
+        ctx.set_materialize_grads(False)
+        y, r, stats = _block_fwd(x, weight, gate, residual, next_weight, scale, eps, True)
+        ctx.numbers, ctx.added = (scale, eps), residual is not None
+        # the stream is read again only for the norm of it
+        ctx.save_for_backward(x, weight, gate, residual if next_weight is not None else None, next_weight, stats)
+        return y, r
+
+    @staticmethod
+    def backward(ctx, dy, dr):
+        _once()
+        x, weight, gate, residual, next_weight, stats = ctx.saved_tensors
+        shape, where = x.shape, x.device
+        dy, dr = _grad(dy, x), _grad(dr, x)
+        new = lambda like: None if like is None else _empty(like.shape, dtype=like.dtype, device=where)  # noqa: E731
+        dx, dweight, dgate, dresidual, dnext = (new(v) for v in (x, weight, gate, residual, next_weight))
+        head = _block_head(x, weight, gate, residual, next_weight, *ctx.numbers)
+        lib = _calls()
+        size = lib.gdr_block_norm_bwd_workspace_size(head[5], head[6])
+        ws = _empty(size, dtype=torch.uint8, device=where)
+        _run(lib.gdr_block_norm_bwd,
+             _BLOCK_NORM.pack(*head, 0, 0, stats.data_ptr(), _ptr(dr), _ptr(dy), dx.data_ptr(), _ptr(dgate), _ptr(dresidual),
+                              dweight.data_ptr(), _ptr(dnext), ws.data_ptr(), size), x.get_device())
+        if ctx.added and next_weight is None:
+            dresidual = dr
+        return dx, dweight, dgate, dresidual, dnext, None, None
+
+
+def gated_residual_rms_norm(x, weight, gate=None, residual=None, next_weight=None, scale=1.0, eps=1e-6):
+    """The norm of a block's output x, times silu of the block's gate, scaled and added to the residual stream, and the
+    norm before the next block, each but the first optional:
+
+        r = residual + scale x / sqrt(mean(x^2) + eps) weight silu(gate),    y = r / sqrt(mean(r^2) + eps) next_weight.
+
+    x, gate, residual [..., D] of one dtype; weight, next_weight [D] fp32; D at most 16384; y is the norm of r before it
+    is rounded.  Without residual and next_weight this is the gated norm of each head of a mixer's output.  Returns
+    (y or None, r); differentiable in every tensor, through y and r."""
+    _no_tangents("gated_residual_rms_norm", x, weight, gate, residual, next_weight)
+    scale, eps = float(scale), float(eps)
+    if _wants_grad(x, weight, gate, residual, next_weight):
+        return _GatedResidualRmsNorm.apply(x, weight, gate, residual, next_weight, scale, eps)
+    return _block_fwd(x, weight, gate, residual, next_weight, scale, eps, False)[:2]
 
 
 # ---- block-scaled 8-bit product ----------------------------------------------

@@ -322,6 +322,71 @@ typedef struct {
 } gdr_ssm_step_args;
 GDR_API int gdr_ssm_step(const gdr_ssm_step_args *args, void *stream);
 
+/* Gated linear recurrence, one state a channel.  For every sequence and
+ * channel, with s = decay_scale softplus(decay):
+ *     a_t = e^{-s sigmoid(decay_gate_t)},
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t,   y_t = h_t silu(z_t) (or h_t).
+ * `states` (nullable) keeps h before every GDR_LINEAR_STRIDE-th token of every
+ * batch row for the backward. */
+#define GDR_LINEAR_STRIDE 64
+typedef struct {
+    const void *x, *input_gate, *decay_gate, *z; /* [B, T, D]; z nullable */
+    const float *decay;         /* [D] */
+    const float *h0;            /* [n_seqs, D], nullable */
+    const int32_t *cu_seqlens;
+    long long B, T, D, n_seqs;
+    long long x_row, x_batch, i_row, i_batch, r_row, r_batch, z_row, z_batch; /* i: input_gate, r: decay_gate */
+    float decay_scale;          /* positive */
+    int dtype;
+    void *y;                    /* [B, T, D] (forward) */
+    float *ht;                  /* [n_seqs, D], nullable (forward) */
+    float *states;              /* [B, ceil(T / 64), D]: written by the forward, read by the backward */
+    /* backward */
+    const void *dy;             /* [B, T, D] contiguous */
+    const float *dht;           /* nullable */
+    void *dx, *di, *dr, *dz;    /* [B, T, D]: of x, input_gate, decay_gate, z; dz iff z */
+    float *ddecay;
+    float *dh0;                 /* nullable */
+    void *workspace;            /* gdr_linear_*_workspace_size bytes, 16-byte aligned (may be null when 0) */
+    size_t workspace_bytes;
+} gdr_linear_args;
+GDR_API size_t gdr_linear_fwd_workspace_size(long long B, long long T, long long D);
+GDR_API int gdr_linear_fwd(const gdr_linear_args *args, void *stream);
+GDR_API size_t gdr_linear_bwd_workspace_size(long long B, long long T, long long D);
+GDR_API int gdr_linear_bwd(const gdr_linear_args *args, void *stream);
+
+/* One token for each of `rows` sequences; slots as in gdr_conv_step. */
+typedef struct {
+    const void *x, *input_gate, *decay_gate, *z; /* [rows, D]; z nullable */
+    const float *decay;
+    float *state;               /* [n_slots, D] */
+    const int32_t *slots;
+    long long rows, D, n_slots, x_row, i_row, r_row, z_row;
+    float decay_scale;
+    int dtype;
+    void *y;                    /* [rows, D] */
+} gdr_linear_step_args;
+GDR_API int gdr_linear_step(const gdr_linear_step_args *args, void *stream);
+
+/* One token for each of `rows` sequences through the gated delta rule (gdr_fwd's
+ * recurrence and state), with h the state of a row's slot and qk-head
+ * hq = hv / (Hv / Hq):
+ *     h <- e^g h,   w = beta (v - h^T k),   h <- h + k w^T,   o = scale h^T q.
+ * K in {64, 128, 192}, V in {64, 128, 192, 256}; slots as in gdr_conv_step.
+ * state is 16-byte aligned. */
+typedef struct {
+    const void *q, *k, *v;      /* [rows, Hq, K] twice, [rows, Hv, V]; heads contiguous */
+    const float *g, *beta;      /* [rows, Hv] */
+    float *state;               /* [n_slots, Hv, K, V] */
+    const int32_t *slots;       /* [rows], nullable */
+    long long rows, Hq, Hv, n_slots, q_row, k_row, v_row;
+    int K, V;
+    float scale;
+    int dtype;
+    void *o;                    /* [rows, Hv, V] */
+} gdr_delta_step_args;
+GDR_API int gdr_delta_step(const gdr_delta_step_args *args, void *stream);
+
 /* Root-mean-square norm of a residual stream:
  *     r = x + residual (rounded to `dtype`; r = x when residual is null),
  *     y = r rsqrt(mean(r^2) + eps) weight.
@@ -358,6 +423,33 @@ typedef struct {
 } gdr_norm_bwd_args;
 GDR_API size_t gdr_norm_bwd_workspace_size(long long M, long long D);
 GDR_API int gdr_norm_bwd(const gdr_norm_bwd_args *args, void *stream);
+
+/* The norm after a block, with the block's gate, the residual stream and the
+ * norm before the next block, each but the first optional:
+ *     u = x rsqrt(mean(x^2) + eps) weight silu(gate),
+ *     r = residual + scale u   (scale u without residual),
+ *     y = r rsqrt(mean(r^2) + eps) next_weight   (r before it is rounded to `dtype`).
+ * `stats` (nullable) keeps the two reciprocal roots of every row for the backward. */
+typedef struct {
+    const void *x, *gate, *residual; /* [M, D], x_row, gate_row, residual_row; gate and residual nullable */
+    const float *weight, *next_weight; /* [D]; next_weight nullable */
+    long long M, D, x_row, gate_row, residual_row;
+    float scale, eps;
+    int dtype;
+    void *r;                    /* [M, D] */
+    void *y;                    /* [M, D]; iff next_weight */
+    float *stats;               /* [M, 2]: written by the forward, read by the backward */
+    /* backward: gradients of r (nullable) and y (nullable); of x, gate, residual, weight, next_weight.  Without
+     * next_weight the gradient of residual is that of r, and dresidual is null. */
+    const void *dr, *dy;        /* [M, D] contiguous */
+    void *dx, *dgate, *dresidual; /* dgate iff gate; dresidual iff residual and next_weight */
+    float *dweight, *dnext_weight; /* dnext_weight iff next_weight */
+    void *workspace;            /* gdr_block_norm_bwd_workspace_size bytes, 16-byte aligned */
+    size_t workspace_bytes;
+} gdr_block_norm_args;
+GDR_API int gdr_block_norm_fwd(const gdr_block_norm_args *args, void *stream);
+GDR_API size_t gdr_block_norm_bwd_workspace_size(long long M, long long D);
+GDR_API int gdr_block_norm_bwd(const gdr_block_norm_args *args, void *stream);
 
 /* out[m, n] = sum_kb a_scales[kb, m] b_scales[n / 128, kb] sum_{k in block kb} a[m, k] b[n, k]:
  * e4m3 operands, blocks of 128 along k (the last may be short), sums in fp32.
