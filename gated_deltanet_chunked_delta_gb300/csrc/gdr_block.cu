@@ -25,9 +25,20 @@ struct BlockP {
     const float *weight, *next;
     void *r, *y, *dx, *dgate, *dres;
     float *stats, *part;  // part: [CTAs, 2, D], the sums of dw and dw'
-    long long M, x_row, gate_row, res_row;
-    int D, lanes;  // lanes: threads of a row
+    long long M, x_row, x_outer, gate_row, gate_outer, res_row, res_outer;
+    int D, lanes, inner;  // lanes: threads of a row
     float scale, eps;
+};
+
+// Where a row of x, gate and residual begins: `inner` heads of a token have a stride of their own.
+struct Row {
+    long long outer, head;
+    __device__ __forceinline__ Row(long long row, int inner) {
+        const unsigned r = (unsigned)row, n = (unsigned)inner, o = r / n;  // fewer than 2^31 rows
+        outer = o;
+        head = r - o * n;
+    }
+    __device__ __forceinline__ long long at(long long row_stride, long long outer_stride) const { return outer * outer_stride + head * row_stride; }
 };
 
 // A thread's kN elements of a row: vectors of eight (kV = 8: rows begin on
@@ -125,9 +136,10 @@ __global__ void __launch_bounds__(kThreads) k_block_fwd(const BlockP p) {
     const bool on = row < p.M;  // lanes of rows past the last only join the shuffles
     typename P::Raw rx, rg, rr;
     const int len = on ? D : 0;
-    P::load(static_cast<const T *>(p.x) + row * p.x_row, len, tid, p.lanes, rx);
-    if (p.gate) P::load(static_cast<const T *>(p.gate) + row * p.gate_row, len, tid, p.lanes, rg);
-    if (p.residual) P::load(static_cast<const T *>(p.residual) + row * p.res_row, len, tid, p.lanes, rr);
+    const Row from(row, p.inner);
+    P::load(static_cast<const T *>(p.x) + from.at(p.x_row, p.x_outer), len, tid, p.lanes, rx);
+    if (p.gate) P::load(static_cast<const T *>(p.gate) + from.at(p.gate_row, p.gate_outer), len, tid, p.lanes, rg);
+    if (p.residual) P::load(static_cast<const T *>(p.residual) + from.at(p.res_row, p.res_outer), len, tid, p.lanes, rr);
     float v[kN], sum[1] = {0.f};
     P::get(rx, v);
 #pragma unroll
@@ -185,11 +197,12 @@ __global__ void __launch_bounds__(kThreads) k_block_bwd(const BlockP p) {
         const long long row = first + (kCta ? 0 : threadIdx.x / p.lanes);
         const int len = row < p.M ? D : 0;
         typename P::Raw rx, rg, rr, ru, ry;
-        P::load(static_cast<const T *>(p.x) + row * p.x_row, len, tid, p.lanes, rx);
-        if (p.gate) P::load(static_cast<const T *>(p.gate) + row * p.gate_row, len, tid, p.lanes, rg);
+        const Row from(row, p.inner);
+        P::load(static_cast<const T *>(p.x) + from.at(p.x_row, p.x_outer), len, tid, p.lanes, rx);
+        if (p.gate) P::load(static_cast<const T *>(p.gate) + from.at(p.gate_row, p.gate_outer), len, tid, p.lanes, rg);
         if (p.dr) P::load(static_cast<const T *>(p.dr) + row * D, len, tid, p.lanes, ru);
         if (p.next) {
-            if (p.residual) P::load(static_cast<const T *>(p.residual) + row * p.res_row, len, tid, p.lanes, rr);
+            if (p.residual) P::load(static_cast<const T *>(p.residual) + from.at(p.res_row, p.res_outer), len, tid, p.lanes, rr);
             if (p.dy) P::load(static_cast<const T *>(p.dy) + row * D, len, tid, p.lanes, ry);
         }
         const float2 inv = len ? *reinterpret_cast<const float2 *>(p.stats + 2 * row) : make_float2(0.f, 0.f);
@@ -346,6 +359,8 @@ int block_common(const gdr_block_norm_args *a, bool bwd) {
     if (a->M < 0 || a->D < 1) return layer_fail(GDR_ERR_SHAPE, "block norm: M must be >= 0 and D >= 1 (got %lld, %lld)", a->M, a->D);
     if (a->D > kMaxD) return layer_fail(GDR_ERR_SHAPE, "block norm: D must be at most %d (got %lld)", kMaxD, a->D);
     if (a->M >= (1LL << 31)) return layer_fail(GDR_ERR_SHAPE, "block norm: too many rows");
+    if (a->inner < 1 || a->inner >= (1LL << 31) || a->M % a->inner)
+        return layer_fail(GDR_ERR_SHAPE, "block norm: M (%lld) must be a multiple of inner (%lld), which is at least 1", a->M, a->inner);
     if (a->dtype != GDR_BF16 && a->dtype != GDR_F32) return layer_fail(GDR_ERR_DTYPE, "block norm: unknown dtype %d", a->dtype);
     const unsigned e = a->dtype == GDR_BF16 ? 2 : 4;
     const bool any = a->M > 0;
@@ -362,7 +377,8 @@ int block_common(const gdr_block_norm_args *a, bool bwd) {
 
 // Whether rows of every tensor are whole vectors on 16-byte boundaries.
 bool block_vec(const gdr_block_norm_args *a) {
-    for (long long v : {a->D, a->x_row, a->gate ? a->gate_row : 0, a->residual ? a->residual_row : 0})
+    for (long long v : {a->D, a->x_row, a->x_outer, a->gate ? a->gate_row : 0, a->gate ? a->gate_outer : 0, a->residual ? a->residual_row : 0,
+                        a->residual ? a->residual_outer : 0})
         if (v % 8) return false;
     for (const void *p : {a->x, a->gate, a->residual, a->dr, a->dy, static_cast<const void *>(a->weight), static_cast<const void *>(a->next_weight),
                           static_cast<const void *>(a->r), static_cast<const void *>(a->y), static_cast<const void *>(a->dx),
@@ -378,7 +394,8 @@ BlockP block_fill(const gdr_block_norm_args *a, const BlockPlan &pl) {
     p.r = a->r; p.y = a->y; p.dx = a->dx; p.dgate = a->dgate; p.dres = a->next_weight ? a->dresidual : nullptr;
     p.stats = a->stats; p.part = static_cast<float *>(a->workspace);
     p.M = a->M; p.x_row = a->x_row; p.gate_row = a->gate_row; p.res_row = a->residual_row;
-    p.D = (int)a->D; p.lanes = pl.lanes;
+    p.x_outer = a->x_outer; p.gate_outer = a->gate_outer; p.res_outer = a->residual_outer;
+    p.D = (int)a->D; p.lanes = pl.lanes; p.inner = (int)a->inner;
     p.scale = a->scale; p.eps = a->eps;
     return p;
 }

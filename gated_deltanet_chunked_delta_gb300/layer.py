@@ -90,7 +90,7 @@ _DELTA_STEP = _Args("gdr_delta_step_args", [
     ("p", "q k v g beta state slots"), ("l", "rows Hq Hv n_slots q_row k_row v_row"), ("i", "K V"), ("f", "scale"),
     ("i", "dtype"), ("p", "o")])
 _BLOCK_NORM = _Args("gdr_block_norm_args", [
-    ("p", "x gate residual weight next_weight"), ("l", "M D x_row gate_row residual_row"), ("f", "scale eps"), ("i", "dtype"),
+    ("p", "x gate residual weight next_weight"), ("l", "M D inner x_row x_outer gate_row gate_outer residual_row residual_outer"), ("f", "scale eps"), ("i", "dtype"),
     ("p", "r y stats dr dy dx dgate dresidual dweight dnext_weight workspace"), ("z", "workspace_bytes")])
 _FP8 = _Args("gdr_fp8_args", [("p", "a b a_scales b_scales"), ("l", "M N K"), ("i", "out_dtype"), ("p", "out")])
 _ConvArgs, _ConvStepArgs, _SsmArgs, _SsmStepArgs, _NormArgs, _NormBwdArgs, _Fp8Args = (
@@ -727,13 +727,26 @@ def residual_rms_norm_fp8(x, weight, residual=None, eps=1e-6):
 # ---- norm after a block --------------------------------------------------------
 
 
+def _head_rows(name, t, inner, d):
+    """[..., D] as [tokens, inner, D]; without heads (inner 1) a token is a row."""
+    try:
+        return t.view(-1, inner, d)
+    except RuntimeError:
+        _fail(1, f"{name} must be rows of one stride, or tokens and heads of one stride each")
+
+
 def _block_head(x, weight, gate, residual, next_weight, scale, eps):
-    """The first 13 fields of the block norm's arguments."""
-    d = x.shape[-1]
-    x2 = _rows("x", x, d)
-    g2, r2 = (None if t is None else _rows(n, t, d) for n, t in (("gate", gate), ("residual", residual)))
-    return (x2.data_ptr(), _ptr(g2), _ptr(r2), weight.data_ptr(), _ptr(next_weight), x2.shape[0], d, x2.stride(0),
-            0 if g2 is None else g2.stride(0), 0 if r2 is None else r2.stride(0), scale, eps, _DTYPES[x.dtype])
+    """The first 17 fields of the block norm's arguments."""
+    d, m, inner = x.shape[-1], x.numel() // x.shape[-1], 1
+    given = [t for t in (x, gate, residual) if t is not None]
+    if x.dim() > 2 and m > 1 and not all(t.is_contiguous() for t in given):
+        inner = x.shape[-2]
+    parts = []
+    for name, t in (("x", x), ("gate", gate), ("residual", residual)):
+        t = None if t is None else _head_rows(name, t, inner, d)
+        parts.append((0, 0, 0) if t is None else (t.data_ptr(), t.stride(1) if inner > 1 else 0, t.stride(0)))
+    return (parts[0][0], parts[1][0], parts[2][0], weight.data_ptr(), _ptr(next_weight), m, d, inner, *parts[0][1:], *parts[1][1:],
+            *parts[2][1:], scale, eps, _DTYPES[x.dtype])
 
 
 def _block_fwd(x, weight, gate, residual, next_weight, scale, eps, keep):
@@ -794,8 +807,8 @@ def gated_residual_rms_norm(x, weight, gate=None, residual=None, next_weight=Non
 
         r = residual + scale x / sqrt(mean(x^2) + eps) weight silu(gate),    y = r / sqrt(mean(r^2) + eps) next_weight.
 
-    x, gate, residual [..., D] of one dtype; weight, next_weight [D] fp32; D at most 16384; y is the norm of r before it
-    is rounded.  Without residual and next_weight this is the gated norm of each head of a mixer's output.  Returns
+    x, gate, residual [..., D] of one dtype, rows of one stride, or [..., heads, D] of one stride for tokens and one for
+    heads (a slice of a projection); weight, next_weight [D] fp32; D at most 16384; y is the norm of r before it is rounded.  Without residual and next_weight this is the gated norm of each head of a mixer's output.  Returns
     (y or None, r); differentiable in every tensor, through y and r."""
     _no_tangents("gated_residual_rms_norm", x, weight, gate, residual, next_weight)
     scale, eps = float(scale), float(eps)

@@ -431,9 +431,11 @@ GDR_API int gdr_norm_bwd(const gdr_norm_bwd_args *args, void *stream);
  *     y = r rsqrt(mean(r^2) + eps) next_weight   (r before it is rounded to `dtype`).
  * `stats` (nullable) keeps the two reciprocal roots of every row for the backward. */
 typedef struct {
-    const void *x, *gate, *residual; /* [M, D], x_row, gate_row, residual_row; gate and residual nullable */
+    /* [M, D]; gate and residual nullable.  Row m lies at (m / inner) *_outer + (m % inner) *_row: `inner` heads of a
+     * token, each a row (1: rows *_outer apart). */
+    const void *x, *gate, *residual;
     const float *weight, *next_weight; /* [D]; next_weight nullable */
-    long long M, D, x_row, gate_row, residual_row;
+    long long M, D, inner, x_row, x_outer, gate_row, gate_outer, residual_row, residual_outer;
     float scale, eps;
     int dtype;
     void *r;                    /* [M, D] */
