@@ -59,12 +59,14 @@ def test_linear_backward_refusals(lib, kw, code):
 
 def test_linear_workspace_sizes(lib):
     for f, a in ((lib.gdr_linear_fwd_workspace_size, lib.gdr_linear_fwd), (lib.gdr_linear_bwd_workspace_size, lib.gdr_linear_bwd)):
-        need = f(1, 5000, 100)
-        assert need >= 16 * 100 * -(-5000 // 128) and need % 16 == 0
-        assert _call(a, _linear(T=5000, D=100, workspace_bytes=need - 1)) == WORKSPACE
-        assert f(0, 5, 5) == f(1, -1, 5) == f(1, 5, 0) == 0
-        assert f(1, 1 << 20, 1 << 12) > 1 << 29
-    assert lib.gdr_linear_fwd_workspace_size(1, 1, 100) == 0  # one chunk needs none
+        for dtype in (0, 1):
+            need = f(1, 5000, 100, dtype)
+            assert need >= 16 * 100 * -(-5000 // 128) and need % 16 == 0
+            assert _call(a, _linear(T=5000, D=100, workspace_bytes=need - 1, dtype=dtype)) == WORKSPACE
+            assert f(0, 5, 5, dtype) == f(1, -1, 5, dtype) == f(1, 5, 0, dtype) == 0
+            assert f(1, 1 << 20, 1 << 12, dtype) > 1 << 29
+            assert lib.gdr_linear_fwd_workspace_size(1, 1, 100, dtype) == 0  # one chunk needs none
+        assert f(1, 5, 5, 2) == 0
 
 
 def _step(cls, **kw):
