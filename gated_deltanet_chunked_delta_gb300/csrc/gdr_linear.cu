@@ -31,23 +31,15 @@ namespace {
 __device__ unsigned g_linear_status;
 
 constexpr int kTile = 64;     // channels of a CTA
-constexpr int kWindow = 4;    // chunks looked back at once
+constexpr int kWindow = 8;    // chunks looked back at once
 constexpr int kPolls = 1 << 20;  // of the records before a chunk, before its wait is given up
-constexpr int kHelpers = 2;   // warps beside those with tokens: one publishes, one looks back
+constexpr int kHelpers = 3;   // warps beside those with tokens: one publishes, one looks back, one scouts
 
-// Tokens of a warp and the warps with tokens of a full chunk.  Two CTAs an SM,
-// each with the tile that it works on and the next one in shared memory.  Long
-// runs: what a warp does once a tile costs as much as two tokens.
-template <typename T, bool kBack>
-struct Shape {
-    static constexpr bool kHalf = sizeof(T) == 2;
-    static constexpr int kRun = kBack ? (kHalf ? 8 : 4) : (kHalf ? 16 : 8);
-    static constexpr int kWarps = 6, kChunk = kRun * kWarps;
-    static constexpr int kThreads = 32 * (kWarps + kHelpers), kCtas = 2;
-    static constexpr int kStride = kHalf ? GDR_LINEAR_STRIDE_BF16 : GDR_LINEAR_STRIDE_F32;  // tokens between the states kept
-    static_assert(!kBack || kChunk == kStride, "the backward's chunks begin at kept states");
-    static_assert(kBack || kStride % kRun == 0, "a run of the forward begins at every one");
-};
+// The warps with tokens of a full chunk, and their tokens.
+constexpr int kWarps = 12, kFwdRun = 8, kBwdRun = 4;
+constexpr int kThreads = 32 * (kWarps + kHelpers), kRegs = 128;  // one full CTA an SM: 480 x 128 registers
+static_assert(kWarps * kBwdRun == GDR_LINEAR_STRIDE, "the backward's chunks begin at kept states");
+static_assert(GDR_LINEAR_STRIDE % kFwdRun == 0, "a run of the forward begins at every one");
 
 struct LinP {
     const void *x, *i, *r, *z, *dy;
@@ -165,31 +157,23 @@ __device__ __forceinline__ bool look_back(const float4 *mine, int ordinal, float
     const int reach = min(kWindow, ordinal);
     for (int polls = 0; polls < kPolls; ++polls) {
         Rec rec[kWindow][2];
-        rec[0][0] = read_rec(mine - kTile);
-        rec[0][1] = read_rec(mine - kTile + 1);
-        const uint32_t near = min(rec[0][0].flag, rec[0][1].flag);
-        if (__all_sync(0xffffffffu, near == 2)) {
-            h[0] = rec[0][0].h;
-            h[1] = rec[0][1].h;
-            return true;
-        }
-        if (!__all_sync(0xffffffffu, near >= 1)) {
-            __nanosleep(60);
-            continue;
-        }
 #pragma unroll
-        for (int j = 1; j < kWindow; ++j)
+        for (int j = 0; j < kWindow; ++j)
 #pragma unroll
             for (int c = 0; c < 2; ++c) rec[j][c] = j < reach ? read_rec(mine - (j + 1) * kTile + c) : Rec{0.f, 0.f, 0.f, 0};
         int from = -1;
         bool open = true;  // every chunk nearer than j has its a and b
 #pragma unroll
-        for (int j = 1; j < kWindow; ++j) {
-            const uint32_t flag = min(rec[j][0].flag, rec[j][1].flag);
-            if (open && from < 0 && __all_sync(0xffffffffu, flag == 2)) from = j;
-            open = open && __all_sync(0xffffffffu, flag >= 1);
+        for (int j = 0; j < kWindow; ++j)
+            if (open && from < 0) {
+                const uint32_t flag = min(rec[j][0].flag, rec[j][1].flag);
+                if (__all_sync(0xffffffffu, flag == 2)) from = j;
+                open = __all_sync(0xffffffffu, flag >= 1);
+            }
+        if (from < 0) {
+            __nanosleep(20);
+            continue;
         }
-        if (from < 0) continue;
 #pragma unroll
         for (int j = kWindow - 1; j >= 0; --j)
 #pragma unroll
@@ -328,36 +312,6 @@ __device__ __forceinline__ void store_f(float *p, f32x2 v, int n) {
     if (n > 1) p[1] = b;
 }
 
-// Sequences that the kRun tokens from t0 on start and end: lane j has token t0 + j's (-1: none).
-template <int kRun>
-__device__ __forceinline__ void mark(const Seqs &q, int t0, int &first, int &last) {
-    const int lane = threadIdx.x % 32, n = q.count();
-    int lo = 0, hi = n - 1;  // the sequence of t0 is one of these
-    while (hi - lo >= 32) {
-        const int step = (hi - lo + 31) / 32;
-        const int below = __popc(__ballot_sync(0xffffffffu, q.bound(min(lo + (lane + 1) * step, hi)) <= t0));
-        const int from = lo;
-        lo = min(from + below * step, hi);
-        if (below < 32) hi = max(lo, min(from + (below + 1) * step, hi) - 1);
-    }
-    lo += max(0, __popc(__ballot_sync(0xffffffffu, lo + lane <= hi && q.bound(min(lo + lane, n)) <= t0)) - 1);
-    const int bound = lo + lane < n ? q.bound(lo + lane) : 0x7fffffff;
-    int mine = lo;
-    bool all = false;
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-        const int below = __popc(__ballot_sync(0xffffffffu, bound <= t0 + j));
-        if (lane == j) mine = lo + max(0, below - 1);
-        all = all || below == 32;
-    }
-    const int t = t0 + lane;
-    first = last = -1;
-    if (lane < kRun && t < q.T) {
-        if (all) mine = q.find(t);  // 32 sequences and more start in this run (all but a few without tokens)
-        if (q.bound(mine) == t) first = mine;
-        if (q.bound(mine + 1) == t + 1) last = mine;
-    }
-}
 // The bounds are meant to rise from 0 to T: one warp looks them over.
 __device__ __forceinline__ void check(const Seqs &s) {
     for (int q = threadIdx.x % 32; q <= s.n; q += 32) {
@@ -379,40 +333,51 @@ __device__ __forceinline__ void pass_empty(const LinP &p, const float *from, flo
     }
 }
 
-// Named barriers of a CTA (0 is __syncthreads'): kReady, the warps' (a, b) are
-// there; kState, the state before the chunk is there; kSums, the sums of G are.
-enum { kReady = 1, kState = 2, kSums = 3 };
+// Named barriers of a CTA (0 is __syncthreads'), two of each kind, for tiles by
+// turns: the warps' (a, b) are there; the chunk's are; the state before the chunk
+// is; the sums of G are.
+enum { kReady = 1, kTotal = 3, kState = 5, kSums = 7 };
 __device__ __forceinline__ void bar_sync(int id, int warps) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id, int warps) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(32 * warps) : "memory"); }
 
-// A tile as the warps work on it: laid out by the warp that looks back, two tiles
-// ahead of its turn.
+// A tile as the warps work on it: laid out by the warp that scouts, three tiles
+// ahead.
+template <int kTok>
 struct Info {
-    float2 s[32];  // s of the lanes' channels (0 behind the last)
-    long long rec; // of the tile's first record
+    float2 s[32];                // s of the lanes' channels (0 behind the last)
+    int first[kTok], last[kTok]; // packed: the sequence that a token starts, ends, or -1
+    long long rec;               // of the tile's first record
     int tile, b, d0, chunk, ordinal, col, small;
 };
-// What the warps of a CTA tell one another; by turns, so that a warp that runs
-// ahead writes where nobody reads any more.
-template <int kWarps>
+constexpr int kInfos = 8;  // tiles k - 2 .. k + 3 are in use at once
+// What the warps of a CTA tell one another.  Two of each, for tiles by turns: a
+// warp begins the tile after the next only when all have the state of this one.
+template <int kTok>
 struct Talk {
-    Info info[4];
+    Info<kTok> info[kInfos];
     float2 a[2][kWarps][32], b[2][kWarps][32];  // the warps' actions, then (from the publisher) those of all warps before
+    float2 total_a[2][32], total_b[2][32];      // the chunk's
     float2 carry[2][32];                        // the state that comes into the chunk
 };
-template <int kWarps>
 struct BackTalk {
     float2 a[2][kWarps][32], b[2][kWarps][32];  // the warps' actions from the first token on
     float2 start[2][kWarps][32];                // the state before a warp's first token
     float2 sums[2][kWarps][32];                 // sums of G
 };
 
-__device__ __forceinline__ int take(const LinP &p) { return (int)min(atomicAdd(p.ticket, 1u), (unsigned)p.tiles); }
-
+// A CTA's `k`-th tile.  Chunks that wait for one another are taken from the counter, so that what they wait for is
+// being worked on; others are dealt out.  By lane 0 of a warp, each once, in order.
+__device__ __forceinline__ int take(const LinP &p, int k) {
+    if (p.chunks > 1) return (int)min(atomicAdd(p.ticket, 1u), (unsigned)p.tiles);
+    return (int)min((long long)blockIdx.x + (long long)k * gridDim.x, (long long)p.tiles);
+}
 // By one warp.
-template <bool kBack>
-__device__ __forceinline__ void lay_out(const LinP &p, Info &to, int tile) {
+template <bool kBack, bool kPacked, int kTok>
+__device__ __forceinline__ void lay_out(const LinP &p, Info<kTok> &to, int k, int warps, bool more) {
     const int lane = threadIdx.x % 32;
+    int tile = p.tiles;
+    if (lane == 0 && (k == 0 || more)) tile = take(p, k);
+    tile = __shfl_sync(0xffffffffu, tile, 0);
     if (tile >= p.tiles) {
         if (lane == 0) to.tile = p.tiles;
         return;
@@ -422,6 +387,30 @@ __device__ __forceinline__ void lay_out(const LinP &p, Info &to, int tile) {
     const float s0 = nch > 0 ? p.scale * softplusf(p.decay[d]) : 0.f, s1 = nch > 1 ? p.scale * softplusf(p.decay[d + 1]) : 0.f;
     const bool small = __all_sync(0xffffffffu, s0 < 0.25f && s1 < 0.25f);
     to.s[lane] = make_float2(s0, s1);
+    if (kPacked) {
+        const int tokens = warps * (kBack ? kBwdRun : kFwdRun), t0 = (kBack ? p.chunks - 1 - ordinal : ordinal) * tokens, t1 = min(t0 + tokens, p.T);
+        for (int j = lane; j < tokens; j += 32) to.first[j] = to.last[j] = -1;
+        __syncwarp();
+        // the last sequence that starts at or before t0, or one before it
+        int lo = 0, hi = p.seqs.n - 1;
+        while (hi - lo >= 32) {
+            const int step = (hi - lo + 31) / 32;
+            const int below = __popc(__ballot_sync(0xffffffffu, p.seqs.bound(min(lo + (lane + 1) * step, hi)) <= t0));
+            const int from = lo;
+            lo = min(from + below * step, hi);
+            if (below < 32) hi = max(lo, min(from + (below + 1) * step, hi) - 1);
+        }
+        // each lane's sequence leaves its number at its first and last token
+        for (bool more = true; more; lo += 32) {
+            const int q = lo + lane;
+            const int start = q < p.seqs.n ? p.seqs.bound(q) : p.T, end = q < p.seqs.n ? p.seqs.bound(q + 1) : p.T;
+            if (start < end) {
+                if (start >= t0 && start < t1) to.first[start - t0] = q;
+                if (end > t0 && end <= t1) to.last[end - 1 - t0] = q;
+            }
+            more = lo + 32 < p.seqs.n && __any_sync(0xffffffffu, lane == 31 && start < t1);
+        }
+    }
     if (lane == 0) {
         to.tile = tile;
         to.b = b;
@@ -433,254 +422,312 @@ __device__ __forceinline__ void lay_out(const LinP &p, Info &to, int tile) {
         to.rec = ((long long)col * p.chunks + ordinal) * kTile;
     }
 }
-
-// Whether a CTA has more than one tile: then it takes them from the counter, and
-// otherwise too where chunks wait for one another.  Lays out the first two.
-template <bool kBack, int kWarps>
-__device__ __forceinline__ bool begin(const LinP &p, Talk<kWarps> &s, int warps) {
+// Lays out the first three tiles; whether there may be more than one.
+template <bool kBack, bool kPacked, int kTok>
+__device__ __forceinline__ bool begin(const LinP &p, Talk<kTok> &s, int warps) {
     const bool more = (int)gridDim.x < p.tiles;
-    if ((int)threadIdx.x / 32 == warps) {
-        int tile[2] = {(int)blockIdx.x, p.tiles};
-        if (p.chunks > 1) {
-            if (threadIdx.x % 32 == 0) {
-                tile[0] = take(p);
-                if (more) tile[1] = take(p);
-            }
-            tile[0] = __shfl_sync(0xffffffffu, tile[0], 0);
-            tile[1] = __shfl_sync(0xffffffffu, tile[1], 0);
-        }
-        lay_out<kBack>(p, s.info[0], tile[0]);
-        lay_out<kBack>(p, s.info[1], tile[1]);
-    }
+    if ((int)threadIdx.x / 32 == warps + 2)
+        for (int k = 0; k < 3; ++k) lay_out<kBack, kPacked>(p, s.info[k], k, warps, more);
     __syncthreads();
     return more;
 }
 
 // The warp that publishes: the chunk's (A, B) from its warps' actions, in whose
 // place it leaves those of all the warps before (kBack: the last warp acts first).
-template <bool kPacked, bool kBack, int kWarps, typename F>
-__device__ __forceinline__ void publish(const LinP &p, Talk<kWarps> &s, const Info &at, int turn, int warps, F meanwhile) {
+template <bool kPacked, bool kBack, int kTok>
+__device__ __forceinline__ void publish(const LinP &p, Talk<kTok> &s, const Info<kTok> &at, int turn, int warps) {
     const int lane = threadIdx.x % 32;
-    bar_sync(kReady, warps + 1);
-    float2 a = make_float2(1.f, 1.f), b = make_float2(0.f, 0.f);
+    bar_sync(kReady + turn, warps + 1);
     float4 *mine = p.rec + at.rec + 2 * lane;
-    for (int k = 0; k < warps; ++k) {
-        const int v = kBack ? warps - 1 - k : k;
-        const float2 av = s.a[turn][v][lane], bv = s.b[turn][v][lane];
-        s.a[turn][v][lane] = a;
-        s.b[turn][v][lane] = b;
-        b = make_float2(act<kPacked>(av.x, bv.x, b.x), act<kPacked>(av.y, bv.y, b.y));
-        a = make_float2(join<kPacked>(a.x, av.x), join<kPacked>(a.y, av.y));
-    }
-    if (at.ordinal > 0) {
+    float2 av[kWarps], bv[kWarps];  // read at once: one after another their latencies add up
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        if (w < warps) {
+            const int v = kBack ? warps - 1 - w : w;
+            av[w] = s.a[turn][v][lane];
+            bv[w] = s.b[turn][v][lane];
+        }
+    float2 a = make_float2(1.f, 1.f), b = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        if (w < warps) {
+            const float2 a0 = a, b0 = b;
+            b = make_float2(act<kPacked>(av[w].x, bv[w].x, b.x), act<kPacked>(av[w].y, bv[w].y, b.y));
+            a = make_float2(join<kPacked>(a.x, av[w].x), join<kPacked>(a.y, av[w].y));
+            av[w] = a0;
+            bv[w] = b0;
+        }
+    if (at.ordinal > 0 && at.ordinal + 1 < p.chunks) {
         write_rec(mine, a.x, b.x, 0.f, 1);
         write_rec(mine + 1, a.y, b.y, 0.f, 1);
     }
-    meanwhile();
-    bar_sync(kState, warps + kHelpers);
-    if (at.ordinal + 1 < p.chunks) {
-        const float2 h = s.carry[turn][lane];
-        write_rec(mine, a.x, b.x, act<kPacked>(a.x, b.x, h.x), 2);
-        write_rec(mine + 1, a.y, b.y, act<kPacked>(a.y, b.y, h.y), 2);
-    }
+    s.total_a[turn][lane] = a;
+    s.total_b[turn][lane] = b;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        if (w < warps) {
+            const int v = kBack ? warps - 1 - w : w;
+            s.a[turn][v][lane] = av[w];
+            s.b[turn][v][lane] = bv[w];
+        }
 }
 // The warp that looks back; `first` [B, D]: the state before the chunk with ordinal 0 (null: zeros).
-template <bool kPacked, bool kBack, int kWarps>
-__device__ __forceinline__ void receive(const LinP &p, Talk<kWarps> &s, const Info &at, const float *first, int k, int warps, bool more) {
-    const int lane = threadIdx.x % 32, d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d));
-    int after = p.tiles;
-    if (more) {
-        if (lane == 0) after = take(p);
-        after = __shfl_sync(0xffffffffu, after, 0);
+template <bool kPacked, int kTok>
+__device__ __forceinline__ void receive(const LinP &p, Talk<kTok> &s, const float *first, int warps) {
+    const int lane = threadIdx.x % 32;
+    for (int k = 0; s.info[k % kInfos].tile < p.tiles; ++k) {
+        const Info<kTok> &at = s.info[k % kInfos];
+        const int turn = k & 1;
+        float4 *mine = p.rec + at.rec + 2 * lane;
+        float h[2] = {0.f, 0.f};
+        if (at.ordinal > 0) {
+            if (!look_back<kPacked>(mine, at.ordinal, h) && lane == 0) atomicOr(&g_linear_status, kStatusTimeout);
+        } else if (!kPacked && first) {
+            const int d = at.d0 + 2 * lane;
+            un2(load_f(first + (long long)at.b * p.D + d, max(0, min(2, p.D - d))), h[0], h[1]);
+        }
+        bar_sync(kTotal + turn, 3);  // the tile before the last is finished: its state may go
+        s.carry[turn][lane] = make_float2(h[0], h[1]);
+        if (at.ordinal + 1 < p.chunks) {
+            const float2 a = s.total_a[turn][lane], b = s.total_b[turn][lane];
+            write_rec(mine, a.x, b.x, act<kPacked>(a.x, b.x, h[0]), 2);
+            write_rec(mine + 1, a.y, b.y, act<kPacked>(a.y, b.y, h[1]), 2);
+        }
+        bar_arrive(kState + turn, warps + 2);
     }
-    lay_out<kBack>(p, s.info[(k + 2) & 3], after);
-    float h[2] = {0.f, 0.f};
-    if (at.ordinal > 0) {
-        if (!look_back<kPacked>(p.rec + at.rec + 2 * lane, at.ordinal, h) && lane == 0) atomicOr(&g_linear_status, kStatusTimeout);
-    } else if (!kPacked && first) {
-        un2(load_f(first + (long long)at.b * p.D + d, nch), h[0], h[1]);
+}
+// The warp that scouts; sequences without tokens hand on `from` to `to`.
+template <bool kPacked, bool kBack, int kTok>
+__device__ __forceinline__ void scout(const LinP &p, Talk<kTok> &s, const float *from, float *to, int warps, bool more) {
+    for (int k = 0; s.info[k % kInfos].tile < p.tiles; ++k) {
+        const Info<kTok> &at = s.info[k % kInfos];
+        lay_out<kBack, kPacked>(p, s.info[(k + 3) % kInfos], k + 3, warps, more);
+        bar_sync(kTotal + (k & 1), 3);  // keeps it from running further ahead
+        bar_arrive(kState + (k & 1), warps + 2);
+        if (kPacked && at.ordinal == 0) {
+            const int d = at.d0 + 2 * (threadIdx.x % 32);
+            pass_empty(p, from, to, d, max(0, min(2, p.D - d)));
+            if (at.col == 0) check(p.seqs);
+        }
     }
-    s.carry[k & 1][lane] = make_float2(h[0], h[1]);
-    bar_sync(kState, warps + kHelpers);
 }
 
 template <typename T, int kAcc, bool kZ, bool kPacked>
-__global__ void __launch_bounds__(Shape<T, false>::kThreads, Shape<T, false>::kCtas) k_linear_fwd(const __grid_constant__ LinP p) {
+__global__ void __launch_bounds__(kThreads, 1) k_linear_fwd(const __grid_constant__ LinP p) {
     using M = Mem<T, kAcc>;
-    using S = Shape<T, false>;
-    constexpr int kRun = S::kRun, kWarps = S::kWarps, kStep = kRun * M::kRow;
+    constexpr int kRun = kFwdRun, kIn = kZ ? 4 : 3, kStep = kRun * M::kRow;
     extern __shared__ __align__(16) char stages[];
-    __shared__ Talk<kWarps> s;
+    constexpr int kTok = kPacked ? kWarps * kRun : 1;
+    __shared__ Talk<kTok> s;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32 - kHelpers;
-    const bool more = begin<false>(p, s, warps);
-    if (warp >= warps) {
-        for (int k = 0; s.info[k & 3].tile < p.tiles; ++k) {
-            const Info &at = s.info[k & 3];
-            if (warp == warps) publish<kPacked, false>(p, s, at, k & 1, warps, [] {});
-            else receive<kPacked, false>(p, s, at, p.h0, k, warps, more);
-            if (kPacked && at.ordinal == 0) {
-                const int d = at.d0 + 2 * lane;
-                if (warp == warps) pass_empty(p, p.h0, p.ht, d, max(0, min(2, p.D - d)));
-                else if (at.col == 0) check(p.seqs);
-            }
+    const bool more = begin<false, kPacked>(p, s, warps);
+    if (warp == warps) {
+        for (int k = 0; s.info[k % kInfos].tile < p.tiles; ++k) {
+            publish<kPacked, false>(p, s, s.info[k % kInfos], k & 1, warps);
+            bar_arrive(kTotal + (k & 1), 3);
         }
         return;
     }
-    char *const own = stages + warp * 3 * kStep;
-    const int other = more ? warps * 3 * kStep : 0;  // from a tile to the next one's
+    if (warp == warps + 1) return receive<kPacked>(p, s, p.h0, warps);
+    if (warp == warps + 2) return scout<kPacked, false>(p, s, p.h0, p.ht, warps, more);
+    char *const own = stages + warp * kIn * kStep;
+    const int other = more ? warps * kIn * kStep : 0;  // from a tile to the next one's
     const T *const tx = static_cast<const T *>(p.x), *const ti = static_cast<const T *>(p.i), *const tr = static_cast<const T *>(p.r);
-    auto stage = [&](const Info &at, int turn) {
-        if (at.tile < p.tiles) {
+    const T *const tz = static_cast<const T *>(p.z);
+    // The k-th tile, and the output gates of the one before, which are read a turn later.
+    auto stage = [&](int k) {
+        __syncwarp();  // the stage has been read
+        auto copy = [&](const Info<kTok> &at, auto f) {
             const int t0 = (at.chunk * warps + warp) * kRun, rows = p.T - t0, ch = p.D - at.d0;
-            char *to = own + turn * other;
-            auto copy = [&](auto whole) {
+            if (kAcc > 2 && rows >= kRun && ch >= kTile) f(t0, rows, ch, std::true_type{}); else f(t0, rows, ch, std::false_type{});
+        };
+        const Info<kTok> &at = s.info[k % kInfos];
+        if (at.tile < p.tiles)
+            copy(at, [&](int t0, int rows, int ch, auto whole) {
                 constexpr bool W = decltype(whole)::value;
+                char *to = own + (k & 1) * other;
                 M::template stage<kRun, W>(to, tr + at.b * p.r_batch + t0 * p.r_row + at.d0, tr, p.r_row, rows, ch);
                 M::template stage<kRun, W>(to + kStep, ti + at.b * p.i_batch + t0 * p.i_row + at.d0, ti, p.i_row, rows, ch);
                 M::template stage<kRun, W>(to + 2 * kStep, tx + at.b * p.x_batch + t0 * p.x_row + at.d0, tx, p.x_row, rows, ch);
-            };
-            if (kAcc > 2 && rows >= kRun && ch >= kTile) copy(std::true_type{}); else copy(std::false_type{});
+            });
+        if (kZ && k > 0) {
+            const Info<kTok> &before = s.info[(k - 1) % kInfos];
+            if (before.tile < p.tiles)
+                copy(before, [&](int t0, int rows, int ch, auto whole) {
+                    M::template stage<kRun, decltype(whole)::value>(own + (k - 1 & 1) * other + 3 * kStep, tz + before.b * p.z_batch + t0 * p.z_row + before.d0,
+                                                                    tz, p.z_row, rows, ch);
+                });
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int first = -1, last = -1, next_first = -1, next_last = -1;
-    stage(s.info[0], 0);
-    if (kPacked && s.info[0].tile < p.tiles) mark<kRun>(p.seqs, (s.info[0].chunk * warps + warp) * kRun, first, last);
-    for (int k = 0; s.info[k & 3].tile < p.tiles; ++k) {
-        const Info &at = s.info[k & 3], &next = s.info[(k + 1) & 3];
-        const int turn = k & 1;
-        stage(next, turn ^ 1);
-        const int d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), t0 = (at.chunk * warps + warp) * kRun, n = min(kRun, p.T - t0);
+    struct Set {  // a tile between its two passes
+        f32x2 a[kRun], b[kRun];
+    };
+    // Whether one of the warp's tokens is a border.
+    auto border = [&](const int (&mark)[kTok]) { return __any_sync(0xffffffffu, lane < kRun && mark[kPacked ? warp * kRun + lane % kRun : 0] >= 0); };
+    // The warp's action.
+    auto front = [&](int k, Set &o) {
+        const Info<kTok> &at = s.info[k % kInfos];
+        if (at.tile >= p.tiles) return;
+        const int turn = k & 1, d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), t0 = (at.chunk * warps + warp) * kRun;
         const f32x2 sv = mk2(at.s[lane].x, at.s[lane].y), neg_s2 = mul2(sv, p.neg_log2e), two_s = add2(sv, sv);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         const char *in = own + turn * other;
-        f32x2 a[kRun], b[kRun], A = p.one, B = dup(0.f);
+        f32x2 A = p.one, B = dup(0.f);
         bool cut = false;  // a sequence starts in this run
-        auto pass = [&](auto sm) {
+        auto pass = [&](auto sm, auto borders) {
+            constexpr bool C = decltype(borders)::value;
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
                 const long long tt = t0 + j;
                 const f32x2 r = M::get(in + j * M::kRow, kAcc == 2 ? tr + at.b * p.r_batch + tt * p.r_row + at.d0 : nullptr);
                 const f32x2 i = M::get(in + kStep + j * M::kRow, kAcc == 2 ? ti + at.b * p.i_batch + tt * p.i_row + at.d0 : nullptr);
                 const f32x2 x = M::get(in + 2 * kStep + j * M::kRow, kAcc == 2 ? tx + at.b * p.x_batch + tt * p.x_row + at.d0 : nullptr);
-                const f32x2 sr = sigmoid2(p, r);
-                a[j] = decay2(p, sr, neg_s2);
-                const f32x2 m = sqrt_2(rest2<decltype(sm)::value>(p, mul2(sr, two_s), a[j]));
-                b[j] = mul2(m, mul2(sigmoid2(p, i), x));
-                const int q = kPacked ? __shfl_sync(0xffffffffu, first, j) : -1;
-                if (kPacked && q >= 0) {
-                    if (p.h0) b[j] = fma2(a[j], load_f(p.h0 + (long long)q * p.D + d, nch), b[j]);
-                    B = b[j];
+                const f32x2 sr = sigmoid2(p, r), si = sigmoid2(p, i);
+                o.a[j] = decay2(p, sr, neg_s2);
+                const f32x2 m = sqrt_2(rest2<decltype(sm)::value>(p, mul2(sr, two_s), o.a[j]));
+                o.b[j] = mul2(m, mul2(si, x));
+                const int q = C ? at.first[C ? warp * kRun + j : 0] : -1;
+                if (C && q >= 0) {
+                    if (p.h0) o.b[j] = fma2(o.a[j], load_f(p.h0 + (long long)q * p.D + d, nch), o.b[j]);
+                    B = o.b[j];
                     A = p.one;
                     cut = true;
                 } else {
-                    B = fma2(a[j], B, b[j]);
-                    A = mul2(A, a[j]);
+                    B = fma2(o.a[j], B, o.b[j]);
+                    A = mul2(A, o.a[j]);
                 }
             }
         };
-        if (at.small) pass(std::true_type{}); else pass(std::false_type{});
-        {
-            float a0, a1, b0, b1;
-            un2(A, a0, a1);
-            un2(B, b0, b1);
-            s.a[turn][warp][lane] = cut ? make_float2(-1.f, -1.f) : make_float2(a0, a1);
-            s.b[turn][warp][lane] = make_float2(b0, b1);
+        // branches inside a run would keep its tokens' latencies from overlapping
+        if (kPacked && border(at.first)) pass(std::false_type{}, std::integral_constant<bool, kPacked>{});
+        else if (at.small) pass(std::true_type{}, std::false_type{});
+        else pass(std::false_type{}, std::false_type{});
+        float a0, a1, b0, b1;
+        un2(A, a0, a1);
+        un2(B, b0, b1);
+        s.a[turn][warp][lane] = cut ? make_float2(-1.f, -1.f) : make_float2(a0, a1);
+        s.b[turn][warp][lane] = make_float2(b0, b1);
+        bar_arrive(kReady + turn, warps + 1);
+    };
+    // Its states and outputs.
+    auto rear = [&](int k, const Set &o) {
+        const Info<kTok> &at = s.info[k % kInfos];
+        const int turn = k & 1, d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), t0 = (at.chunk * warps + warp) * kRun, n = min(kRun, p.T - t0);
+        // the output gates are of the group before the last; where no next tile's action has waited for it, this does
+        if (kZ) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();
         }
-        bar_arrive(kReady, warps + 1);
-        constexpr int kAhead = kRun < 8 ? kRun : 8;  // z is read in runs of eight
-        f32x2 z[kZ ? kAhead : 1];
-        const T *pz = kZ ? static_cast<const T *>(p.z) + at.b * p.z_batch + t0 * p.z_row + d : nullptr;
-        auto read_z = [&](int from) {
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) z[kZ ? j : 0] = M::load(pz + (from + j) * p.z_row, from + j < n ? nch : 0);
-        };
-        if (kZ) read_z(0);
-        if (kPacked && next.tile < p.tiles) mark<kRun>(p.seqs, (next.chunk * warps + warp) * kRun, next_first, next_last);
-        bar_sync(kState, warps + kHelpers);
+        bar_sync(kState + turn, warps + 2);
         const float2 c = s.carry[turn][lane];
         f32x2 h = act2<kPacked>(s.a[turn][warp][lane], s.b[turn][warp][lane], mk2(c.x, c.y));
         T *py = static_cast<T *>(p.y) + ((long long)at.b * p.T + t0) * p.D + d;
-        float *const pst = p.states + (long long)at.b * ((p.T + S::kStride - 1) / S::kStride) * p.D + d;
-        auto finish = [&](auto whole) {
-            constexpr bool W = decltype(whole)::value;
+        if (p.states && n > 0 && t0 % GDR_LINEAR_STRIDE == 0)
+            store_f(p.states + ((long long)at.b * ((p.T + GDR_LINEAR_STRIDE - 1) / GDR_LINEAR_STRIDE) + t0 / GDR_LINEAR_STRIDE) * p.D + d, h, nch);
+        auto finish = [&](auto whole, auto borders) {
+            constexpr bool W = decltype(whole)::value, C = decltype(borders)::value;
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
                 if (W || j < n) {
-                    if (j == 0 && p.states && t0 % S::kStride == 0) store_f(pst + (long long)(t0 / S::kStride) * p.D, h, nch);
-                    const bool start = kPacked && __shfl_sync(0xffffffffu, first, j) >= 0;
-                    h = start ? b[j] : fma2(a[j], h, b[j]);
+                    const bool start = C && at.first[C ? warp * kRun + j : 0] >= 0;
+                    h = start ? o.b[j] : fma2(o.a[j], h, o.b[j]);
                     f32x2 y = h;
                     if (kZ) {
-                        if (j && j % kAhead == 0) read_z(j);
-                        y = mul2(h, mul2(z[j % kAhead], sigmoid2(p, z[j % kAhead])));
+                        const f32x2 z = M::get(own + turn * other + 3 * kStep + j * M::kRow,
+                                               kAcc == 2 ? tz + at.b * p.z_batch + (long long)(t0 + j) * p.z_row + at.d0 : nullptr);
+                        y = mul2(h, mul2(z, sigmoid2(p, z)));
                     }
                     M::store(py + (long long)j * p.D, y, W ? 2 : nch);
-                    if (kPacked) {
-                        const int q = __shfl_sync(0xffffffffu, last, j);
+                    if (C) {
+                        const int q = at.last[C ? warp * kRun + j : 0];
                         if (q >= 0 && p.ht) store_f(p.ht + (long long)q * p.D + d, h, nch);
                     }
                 }
             }
             if (!kPacked && p.ht && n > 0 && t0 + n == p.T) store_f(p.ht + (long long)at.b * p.D + d, h, nch);
         };
-        if (n == kRun && p.D - at.d0 >= kTile) finish(std::true_type{}); else finish(std::false_type{});
-        first = next_first;
-        last = next_last;
+        if (kPacked && (border(at.first) || border(at.last))) finish(std::false_type{}, std::integral_constant<bool, kPacked>{});
+        else if (n == kRun && p.D - at.d0 >= kTile) finish(std::true_type{}, std::false_type{});
+        else finish(std::false_type{}, std::false_type{});
+    };
+    // A tile's action is published before the one before it is finished: the state
+    // comes in meanwhile.
+    Set even, odd;
+    stage(0);
+    stage(1);
+    front(0, even);
+    for (int k = 0; s.info[k % kInfos].tile < p.tiles; k += 2) {
+        stage(k + 2);
+        front(k + 1, odd);
+        rear(k, even);
+        if (s.info[(k + 1) % kInfos].tile >= p.tiles) break;
+        stage(k + 3);
+        front(k + 2, even);
+        rear(k + 1, odd);
     }
 }
 
 template <typename T, int kAcc, bool kZ, bool kPacked>
-__global__ void __launch_bounds__(Shape<T, true>::kThreads, Shape<T, true>::kCtas) k_linear_bwd(const __grid_constant__ LinP p) {
+__global__ void __launch_bounds__(kThreads, 1) k_linear_bwd(const __grid_constant__ LinP p) {
     using M = Mem<T, kAcc>;
-    using S = Shape<T, true>;
-    constexpr int kRun = S::kRun, kWarps = S::kWarps, kIn = kZ ? 5 : 4, kStep = kRun * M::kRow;
+    constexpr int kRun = kBwdRun, kIn = kZ ? 5 : 4, kStep = kRun * M::kRow;
     extern __shared__ __align__(16) char stages[];
-    __shared__ Talk<kWarps> s;
-    __shared__ BackTalk<kWarps> f;
+    constexpr int kTok = kPacked ? kWarps * kRun : 1;
+    __shared__ Talk<kTok> s;
+    __shared__ BackTalk f;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32 - kHelpers;
-    const bool more = begin<true>(p, s, warps);
-    if (warp >= warps) {
-        for (int k = 0; s.info[k & 3].tile < p.tiles; ++k) {
-            const Info &at = s.info[k & 3];
+    const bool more = begin<true, kPacked>(p, s, warps);
+    if (warp == warps) {
+        auto sum = [&](int k) {
+            const Info<kTok> &at = s.info[k % kInfos];
+            const int turn = k & 1, d = at.d0 + 2 * lane;
+            bar_sync(kSums + turn, warps + 1);
+            f32x2 g = dup(0.f);
+            for (int v = 0; v < warps; ++v) g = add2(g, mk2(f.sums[turn][v][lane].x, f.sums[turn][v][lane].y));
+            store_f(p.part + ((long long)at.b * p.chunks + at.chunk) * p.D + d, g, max(0, min(2, p.D - d)));
+        };
+        int k = 0;
+        for (; s.info[k % kInfos].tile < p.tiles; ++k) {
+            const Info<kTok> &at = s.info[k % kInfos];
             const int d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), turn = k & 1;
-            if (warp == warps) {
-                f32x2 h = load_f(p.states + ((long long)at.b * p.chunks + at.chunk) * p.D + d, nch);
-                publish<kPacked, true>(p, s, at, turn, warps, [&] {
-                    for (int v = 0; v < warps; ++v) {
-                        float h0, h1;
-                        un2(h, h0, h1);
-                        f.start[turn][v][lane] = make_float2(h0, h1);
-                        h = act2<kPacked>(f.a[turn][v][lane], f.b[turn][v][lane], h);
-                    }
-                });
-                bar_sync(kSums, warps + 1);
-                float2 g = make_float2(0.f, 0.f);
-                for (int v = 0; v < warps; ++v) {
-                    g.x += f.sums[turn][v][lane].x;
-                    g.y += f.sums[turn][v][lane].y;
+            f32x2 h = load_f(p.states + ((long long)at.b * p.chunks + at.chunk) * p.D + d, nch);
+            publish<kPacked, true>(p, s, at, turn, warps);
+            float2 fa[kWarps], fb[kWarps];
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v)
+                if (v < warps) {
+                    fa[v] = f.a[turn][v][lane];
+                    fb[v] = f.b[turn][v][lane];
                 }
-                store_f(p.part + ((long long)at.b * p.chunks + at.chunk) * p.D + d, mk2(g.x, g.y), nch);
-            } else {
-                receive<kPacked, true>(p, s, at, p.dht, k, warps, more);
-            }
-            if (kPacked && at.ordinal == 0) {
-                if (warp == warps) pass_empty(p, p.dht, p.dh0, d, nch);
-                else if (at.col == 0) check(p.seqs);
-            }
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v)
+                if (v < warps) {
+                    float h0, h1;
+                    un2(h, h0, h1);
+                    f.start[turn][v][lane] = make_float2(h0, h1);
+                    h = act2<kPacked>(fa[v], fb[v], h);
+                }
+            bar_arrive(kTotal + turn, 3);
+            if (k > 0) sum(k - 1);
         }
+        if (k > 0) sum(k - 1);
         return;
     }
+    if (warp == warps + 1) return receive<kPacked>(p, s, p.dht, warps);
+    if (warp == warps + 2) return scout<kPacked, true>(p, s, p.dht, p.dh0, warps, more);
     char *const own = stages + warp * kIn * kStep;
-    const int other = more ? warps * kIn * kStep : 0;  // from a tile to the next one's
+    const int other = more ? warps * kIn * kStep : 0;  // from a tile to the next one's, of three
     const T *const tx = static_cast<const T *>(p.x), *const ti = static_cast<const T *>(p.i), *const tr = static_cast<const T *>(p.r);
     const T *const tz = static_cast<const T *>(p.z), *const ty = static_cast<const T *>(p.dy);
     const long long y_batch = (long long)p.T * p.D;
-    auto stage = [&](const Info &at, int turn) {
+    auto stage = [&](int k) {
+        const Info<kTok> &at = s.info[k % kInfos];
+        __syncwarp();  // the stage has been read
         if (at.tile < p.tiles) {
             const int t0 = (at.chunk * warps + warp) * kRun, rows = p.T - t0, ch = p.D - at.d0;
-            char *to = own + turn * other;
+            char *to = own + k % 3 * other;
             auto copy = [&](auto whole) {
                 constexpr bool W = decltype(whole)::value;
                 M::template stage<kRun, W>(to, tr + at.b * p.r_batch + t0 * p.r_row + at.d0, tr, p.r_row, rows, ch);
@@ -693,142 +740,170 @@ __global__ void __launch_bounds__(Shape<T, true>::kThreads, Shape<T, true>::kCta
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int first = -1, last = -1, next_first = -1, next_last = -1;
-    stage(s.info[0], 0);
-    if (kPacked && s.info[0].tile < p.tiles) mark<kRun>(p.seqs, (s.info[0].chunk * warps + warp) * kRun, first, last);
-    for (int k = 0; s.info[k & 3].tile < p.tiles; ++k) {
-        const Info &at = s.info[k & 3], &next = s.info[(k + 1) & 3];
-        const int turn = k & 1;
-        __syncwarp();  // the stage has been read
-        stage(next, turn ^ 1);
-        const int d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), t0 = (at.chunk * warps + warp) * kRun, n = min(kRun, p.T - t0);
-        const f32x2 neg_s = mul2(mk2(at.s[lane].x, at.s[lane].y), p.minus), log2e = mul2(p.neg_log2e, p.minus), neg_s2 = mul2(neg_s, log2e);
+    struct Set {  // a tile between its two passes: a, m sigmoid(i), sigmoid(r), sigmoid(i) a^2 (-L / m)
+        f32x2 a[kRun], mi[kRun], sr[kRun], g[kRun];
+    };
+    auto get = [&](const Info<kTok> &at, const char *in, int which, int j) {
+        const T *from = nullptr;
+        if (kAcc == 2) {
+            const long long tt = (at.chunk * warps + warp) * kRun + j;
+            from = at.d0 + (which == 0 ? tr + at.b * p.r_batch + tt * p.r_row : which == 1 ? ti + at.b * p.i_batch + tt * p.i_row
+                          : which == 2 ? tx + at.b * p.x_batch + tt * p.x_row : which == 3 ? ty + at.b * y_batch + tt * p.D
+                                       : tz + at.b * p.z_batch + tt * p.z_row);
+        }
+        return M::get(in + which * kStep + j * M::kRow, from);
+    };
+    auto din = [&](const Info<kTok> &at, const char *in, int j) {
+        const f32x2 y = get(at, in, 3, j);
+        if (!kZ) return y;
+        const f32x2 z = get(at, in, 4, j);
+        return mul2(y, mul2(z, sigmoid2(p, z)));
+    };
+    // Whether one of the warp's tokens is a border.
+    auto border = [&](const int (&mark)[kTok]) { return __any_sync(0xffffffffu, lane < kRun && mark[kPacked ? warp * kRun + lane % kRun : 0] >= 0); };
+    auto front = [&](int k, Set &o) {
+        const Info<kTok> &at = s.info[k % kInfos];
+        if (at.tile >= p.tiles) return;
+        const int turn = k & 1, d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), t0 = (at.chunk * warps + warp) * kRun, n = min(kRun, p.T - t0);
+        const f32x2 neg_s = mul2(mk2(at.s[lane].x, at.s[lane].y), p.minus), neg_s2 = mul2(mk2(at.s[lane].x, at.s[lane].y), p.neg_log2e);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
-        char *in = own + turn * other;
-        auto get = [&](int which, int j) {
-            const long long tt = t0 + j;
-            const T *from = nullptr;
-            if (kAcc == 2)
-                from = at.d0 + (which == 0 ? tr + at.b * p.r_batch + tt * p.r_row : which == 1 ? ti + at.b * p.i_batch + tt * p.i_row
-                              : which == 2 ? tx + at.b * p.x_batch + tt * p.x_row : which == 3 ? ty + at.b * y_batch + tt * p.D
-                                           : tz + at.b * p.z_batch + tt * p.z_row);
-            return M::get(in + which * kStep + j * M::kRow, from);
-        };
-        auto starts = [&](int j) { return kPacked ? __shfl_sync(0xffffffffu, first, j) : -1; };
-        auto ends = [&](int j) { return kPacked ? __shfl_sync(0xffffffffu, last, j) : -1; };
-        auto given = [&](const float *t, int q) { return t ? load_f(t + (long long)q * p.D + d, nch) : dup(0.f); };
-        auto din = [&](int j) {
-            const f32x2 y = get(3, j);
-            if (!kZ) return y;
-            const f32x2 z = get(4, j);
-            return mul2(y, mul2(z, sigmoid2(p, z)));
-        };
-        // a, m sigmoid(i), sigmoid(r); g: first sigmoid(i) a^2 (-L / m), then G / e.  sigmoid(i) waits
-        // in the place of both gates.
-        f32x2 a[kRun], mi[kRun], sr[kRun], g[kRun], A = p.one, B = dup(0.f);
+        char *in = own + k % 3 * other;
+        f32x2 A = p.one, B = dup(0.f);
         bool cut = false;
-        auto pass = [&](auto sm) {
-#pragma unroll
-            for (int j = 0; j < kRun; ++j) {
-                sr[j] = sigmoid2(p, get(0, j));
-                const f32x2 si = sigmoid2(p, get(1, j));
-                M::put2(in + kStep + j * M::kRow, in + j * M::kRow, si);
-                a[j] = decay2(p, sr[j], neg_s2);
-                const f32x2 L = mul2(sr[j], neg_s), v = mul2(add2(L, L), p.minus);
-                // a gate is not quite closed here (1e-36), so that m has a reciprocal
-                const f32x2 rest = add2(rest2<decltype(sm)::value>(p, v, a[j]), dup(1e-36f)), inv = rsqrt_2(rest);
-                mi[j] = mul2(mul2(rest, inv), si);
-                g[j] = mul2(mul2(mul2(a[j], a[j]), mul2(L, inv)), mul2(si, p.minus));
-                const f32x2 b = mul2(mi[j], get(2, j));
-                const int q = starts(j);
-                if (kPacked && q >= 0) {
-                    B = fma2(a[j], given(p.h0, q), b);
-                    A = p.one;
-                    cut = true;
-                } else {
-                    B = fma2(a[j], B, b);
-                    A = mul2(A, a[j]);
-                }
-            }
-        };
-        if (at.small) pass(std::true_type{}); else pass(std::false_type{});
+        auto given = [&](const float *t, int q) { return t ? load_f(t + (long long)q * p.D + d, nch) : dup(0.f); };
         auto tell = [&](float2 *ta, float2 *tb) {
             float a0, a1, b0, b1;
             un2(A, a0, a1);
             un2(B, b0, b1);
             ta[lane] = cut ? make_float2(-1.f, -1.f) : make_float2(a0, a1);
             tb[lane] = make_float2(b0, b1);
+            A = p.one;
+            B = dup(0.f);
+            cut = false;
         };
-        tell(f.a[turn][warp], f.b[turn][warp]);
-        A = p.one;
-        B = dup(0.f);
-        cut = false;
+        auto pass = [&](auto sm, auto borders) {
+            constexpr bool C = decltype(borders)::value;
 #pragma unroll
-        for (int j = kRun - 1; j >= 0; --j) {
-            if (j < n) {
-                const int q = ends(j);
-                if (kPacked && q >= 0) {
-                    B = given(p.dht, q);
+            for (int j = 0; j < kRun; ++j) {
+                const f32x2 sr = sigmoid2(p, get(at, in, 0, j)), si = sigmoid2(p, get(at, in, 1, j));
+                M::put2(in + kStep + j * M::kRow, in + j * M::kRow, si);  // it waits in the place of both gates
+                const f32x2 a = decay2(p, sr, neg_s2), L = mul2(sr, neg_s), v = mul2(add2(L, L), p.minus);
+                // a gate is not quite closed here (1e-36), so that m has a reciprocal
+                const f32x2 rest = add2(rest2<decltype(sm)::value>(p, v, a), dup(1e-36f)), inv = rsqrt_2(rest);
+                const f32x2 mi = mul2(mul2(rest, inv), si), b = mul2(mi, get(at, in, 2, j));
+                o.a[j] = a;
+                o.mi[j] = mi;
+                o.sr[j] = sr;
+                o.g[j] = mul2(mul2(mul2(a, a), mul2(L, inv)), mul2(si, p.minus));
+                const int q = C ? at.first[C ? warp * kRun + j : 0] : -1;
+                if (C && q >= 0) {
+                    B = fma2(a, given(p.h0, q), b);
                     A = p.one;
                     cut = true;
+                } else {
+                    B = fma2(a, B, b);
+                    A = mul2(A, a);
                 }
-                A = mul2(A, a[j]);
-                B = mul2(a[j], add2(din(j), B));
             }
-        }
+        };
+        // branches inside a run would keep its tokens' latencies from overlapping
+        if (kPacked && border(at.first)) pass(std::false_type{}, std::integral_constant<bool, kPacked>{});
+        else if (at.small) pass(std::true_type{}, std::false_type{});
+        else pass(std::false_type{}, std::false_type{});
+        tell(f.a[turn][warp], f.b[turn][warp]);
+        auto back = [&](auto whole, auto borders) {
+            constexpr bool W = decltype(whole)::value, C = decltype(borders)::value;
+#pragma unroll
+            for (int j = kRun - 1; j >= 0; --j) {
+                if (W || j < n) {
+                    const int q = C ? at.last[C ? warp * kRun + j : 0] : -1;
+                    if (C && q >= 0) {
+                        B = given(p.dht, q);
+                        A = p.one;
+                        cut = true;
+                    }
+                    A = mul2(A, o.a[j]);
+                    B = mul2(o.a[j], add2(din(at, in, j), B));
+                }
+            }
+        };
+        if (kPacked && border(at.last)) back(std::false_type{}, std::integral_constant<bool, kPacked>{});
+        else if (n == kRun) back(std::true_type{}, std::false_type{});
+        else back(std::false_type{}, std::false_type{});
         tell(s.a[turn][warp], s.b[turn][warp]);
-        bar_arrive(kReady, warps + 1);
-        if (kPacked && next.tile < p.tiles) mark<kRun>(p.seqs, (next.chunk * warps + warp) * kRun, next_first, next_last);
-        bar_sync(kState, warps + kHelpers);
+        bar_arrive(kReady + turn, warps + 1);
+    };
+    auto rear = [&](int k, Set &o) {
+        const Info<kTok> &at = s.info[k % kInfos];
+        const int turn = k & 1, d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), t0 = (at.chunk * warps + warp) * kRun, n = min(kRun, p.T - t0);
+        const f32x2 neg_s = mul2(mk2(at.s[lane].x, at.s[lane].y), p.minus);
+        const char *in = own + k % 3 * other;
+        auto given = [&](const float *t, int q) { return t ? load_f(t + (long long)q * p.D + d, nch) : dup(0.f); };
+        bar_sync(kState + turn, warps + 2);
         f32x2 h = mk2(f.start[turn][warp][lane].x, f.start[turn][warp][lane].y), sum = dup(0.f);
         const float2 c = s.carry[turn][lane];
         f32x2 e = act2<kPacked>(s.a[turn][warp][lane], s.b[turn][warp][lane], mk2(c.x, c.y));
         const long long out = ((long long)at.b * p.T + t0) * p.D + d;
         T *const px = static_cast<T *>(p.dx) + out, *const pi = static_cast<T *>(p.di) + out, *const pr = static_cast<T *>(p.dr) + out;
         T *const pz = kZ ? static_cast<T *>(p.dz) + out : nullptr;
-        auto finish = [&](auto whole) {
-            constexpr bool W = decltype(whole)::value;
+        auto finish = [&](auto whole, auto borders) {
+            constexpr bool W = decltype(whole)::value, C = decltype(borders)::value;
+            auto starts = [&](int j) { return C ? at.first[C ? warp * kRun + j : 0] : -1; };
+            auto ends = [&](int j) { return C ? at.last[C ? warp * kRun + j : 0] : -1; };
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) {
+            for (int j = 0; j < kRun; ++j) {  // g becomes G / e
                 const int q = starts(j);
-                if (kPacked && q >= 0) h = given(p.h0, q);
-                const f32x2 x = get(2, j), La = mul2(mul2(sr[j], neg_s), a[j]);
-                g[j] = fma2(La, h, mul2(g[j], x));
-                h = fma2(a[j], h, mul2(mi[j], x));
+                if (C && q >= 0) h = given(p.h0, q);
+                const f32x2 x = get(at, in, 2, j), La = mul2(mul2(o.sr[j], neg_s), o.a[j]);
+                o.g[j] = fma2(La, h, mul2(o.g[j], x));
+                h = fma2(o.a[j], h, mul2(o.mi[j], x));
                 if (kZ && (W || j < n)) {
-                    const f32x2 z = get(4, j), on = sigmoid2(p, z);
+                    const f32x2 z = get(at, in, 4, j), on = sigmoid2(p, z);
                     const f32x2 slope = mul2(on, fma2(z, fma2(on, p.minus, p.one), p.one));
-                    M::store(pz + (long long)j * p.D, mul2(mul2(get(3, j), h), slope), W ? 2 : nch);
+                    M::store(pz + (long long)j * p.D, mul2(mul2(get(at, in, 3, j), h), slope), W ? 2 : nch);
                 }
             }
 #pragma unroll
             for (int j = kRun - 1; j >= 0; --j) {
                 if (W || j < n) {
                     const int q = ends(j);
-                    if (kPacked && q >= 0) e = given(p.dht, q);
-                    e = add2(e, din(j));
-                    const f32x2 G = mul2(e, g[j]), dx = mul2(e, mi[j]), si = M::get2(in + kStep + j * M::kRow, in + j * M::kRow);
+                    if (C && q >= 0) e = given(p.dht, q);
+                    e = add2(e, din(at, in, j));
+                    const f32x2 G = mul2(e, o.g[j]), dx = mul2(e, o.mi[j]), si = M::get2(in + kStep + j * M::kRow, in + j * M::kRow);
                     sum = add2(sum, G);
                     const long long to = (long long)j * p.D;
                     M::store(px + to, dx, W ? 2 : nch);
-                    M::store(pi + to, mul2(mul2(dx, get(2, j)), fma2(si, p.minus, p.one)), W ? 2 : nch);
-                    M::store(pr + to, mul2(G, fma2(sr[j], p.minus, p.one)), W ? 2 : nch);
-                    e = mul2(e, a[j]);
-                    const int o = kPacked ? starts(j) : t0 + j == 0 ? at.b : -1;
-                    if (o >= 0 && p.dh0) store_f(p.dh0 + (long long)o * p.D + d, e, nch);
+                    M::store(pi + to, mul2(mul2(dx, get(at, in, 2, j)), fma2(si, p.minus, p.one)), W ? 2 : nch);
+                    M::store(pr + to, mul2(G, fma2(o.sr[j], p.minus, p.one)), W ? 2 : nch);
+                    e = mul2(e, o.a[j]);
+                    if (kPacked ? C : j == 0) {
+                        const int first = kPacked ? starts(j) : t0 == 0 ? at.b : -1;
+                        if (first >= 0 && p.dh0) store_f(p.dh0 + (long long)first * p.D + d, e, nch);
+                    }
                 }
             }
         };
-        if (n == kRun && p.D - at.d0 >= kTile) finish(std::true_type{}); else finish(std::false_type{});
-        {
-            float g0, g1;
-            un2(sum, g0, g1);
-            f.sums[turn][warp][lane] = make_float2(g0, g1);
-        }
-        bar_arrive(kSums, warps + 1);
-        first = next_first;
-        last = next_last;
+        if (kPacked && (border(at.first) || border(at.last))) finish(std::false_type{}, std::integral_constant<bool, kPacked>{});
+        else if (n == kRun && p.D - at.d0 >= kTile) finish(std::true_type{}, std::false_type{});
+        else finish(std::false_type{}, std::false_type{});
+        float g0, g1;
+        un2(sum, g0, g1);
+        f.sums[turn][warp][lane] = make_float2(g0, g1);
+        bar_arrive(kSums + turn, warps + 1);
+    };
+    Set even, odd;  // as in the forward
+    stage(0);
+    stage(1);
+    front(0, even);
+    for (int k = 0; s.info[k % kInfos].tile < p.tiles; k += 2) {
+        stage(k + 2);
+        front(k + 1, odd);
+        rear(k, even);
+        if (s.info[(k + 1) % kInfos].tile >= p.tiles) break;
+        stage(k + 3);
+        front(k + 2, even);
+        rear(k + 1, odd);
     }
 }
 
@@ -917,14 +992,9 @@ struct LinPlan {
     int warps;  // with tokens, of a CTA
     long long chunks;
 };
-LinPlan linear_plan(long long T, int dtype, bool bwd) {
-    auto of = [&](auto t, auto back) {
-        using S = Shape<decltype(t), decltype(back)::value>;
-        const int run = S::kRun, warps = (int)std::max(1LL, std::min<long long>(S::kWarps, (T + run - 1) / run));
-        return LinPlan{warps, std::max(1LL, (T + warps * run - 1) / (warps * run))};
-    };
-    if (bwd) return dtype == GDR_BF16 ? of(bf16_t{}, std::true_type{}) : of(float{}, std::true_type{});
-    return dtype == GDR_BF16 ? of(bf16_t{}, std::false_type{}) : of(float{}, std::false_type{});
+LinPlan linear_plan(long long T, bool bwd) {
+    const int run = bwd ? kBwdRun : kFwdRun, warps = (int)std::max(1LL, std::min<long long>(kWarps, (T + run - 1) / run));
+    return LinPlan{warps, std::max(1LL, (T + warps * run - 1) / (warps * run))};
 }
 
 // The workspace: the counter and the records (where there is more than one
@@ -932,8 +1002,8 @@ LinPlan linear_plan(long long T, int dtype, bool bwd) {
 struct LinSpace {
     size_t rec, part, total, zeroed;
 };
-LinSpace linear_space(long long B, long long T, long long D, int dtype, bool bwd) {
-    const LinPlan pl = linear_plan(T, dtype, bwd);
+LinSpace linear_space(long long B, long long T, long long D, bool bwd) {
+    const LinPlan pl = linear_plan(T, bwd);
     LinSpace s{};
     size_t off = 0;
     if (pl.chunks > 1) {
@@ -987,7 +1057,7 @@ int linear_access(int dtype, std::initializer_list<const void *> ptrs, std::init
 
 int linear_fill(const gdr_linear_args *a, const Seqs &s, bool bwd, const LinSpace &sp, LinP *p, LinPlan *pl, cudaStream_t st) {
     *p = linear_constants();
-    *pl = linear_plan(a->T, a->dtype, bwd);
+    *pl = linear_plan(a->T, bwd);
     p->x = a->x; p->i = a->input_gate; p->r = a->decay_gate; p->z = a->z; p->dy = a->dy;
     p->decay = a->decay; p->h0 = a->h0; p->dht = a->dht;
     p->y = a->y; p->dx = a->dx; p->di = a->di; p->dr = a->dr; p->dz = a->dz;
@@ -1013,17 +1083,16 @@ int linear_fill(const gdr_linear_args *a, const Seqs &s, bool bwd, const LinSpac
     return GDR_OK;
 }
 
-// As many CTAs as run at once, each with two tiles in shared memory; all tiles at
-// once where they are fewer or do not hand states on.  `each`: a warp's tile.
+// As many CTAs as run at once, with `stages` tiles in shared memory (one where
+// every CTA has but one).  `each`: a warp's part of a tile.
 template <typename K>
-int linear_launch(K *kernel, const LinP &p, const LinPlan &pl, int ctas, size_t each, cudaStream_t st) {
-    const size_t tile = each * pl.warps;
-    long long grid = p.tiles;
-    if (p.chunks > 1) grid = std::min(grid, (long long)layer_sms() * ctas);
-    const size_t smem = grid < p.tiles ? 2 * tile : tile;
+int linear_launch(K *kernel, const LinP &p, const LinPlan &pl, int stages, size_t each, cudaStream_t st) {
+    const int threads = 32 * (pl.warps + kHelpers);
+    const long long grid = std::min<long long>(p.tiles, (long long)layer_sms() * (65536 / (threads * kRegs)));
+    const size_t smem = each * pl.warps * (grid < p.tiles ? stages : 1);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return layer_fail(GDR_ERR_CUDA, "linear scan: %s", cudaGetErrorString(e));
-    kernel<<<(unsigned)grid, 32 * (pl.warps + kHelpers), smem, st>>>(p);
+    kernel<<<(unsigned)grid, threads, smem, st>>>(p);
     return GDR_OK;
 }
 
@@ -1070,12 +1139,12 @@ unsigned linear_take_status(cudaStream_t st) {
 
 extern "C" {
 
-size_t gdr_linear_fwd_workspace_size(long long B, long long T, long long D, int dtype) {
-    return linear_sizes(B, T, D, dtype) ? 0 : linear_space(B, T, D, dtype, false).total;
+size_t gdr_linear_fwd_workspace_size(long long B, long long T, long long D) {
+    return linear_sizes(B, T, D, GDR_BF16) ? 0 : linear_space(B, T, D, false).total;
 }
 
-size_t gdr_linear_bwd_workspace_size(long long B, long long T, long long D, int dtype) {
-    return linear_sizes(B, T, D, dtype) ? 0 : linear_space(B, T, D, dtype, true).total;
+size_t gdr_linear_bwd_workspace_size(long long B, long long T, long long D) {
+    return linear_sizes(B, T, D, GDR_BF16) ? 0 : linear_space(B, T, D, true).total;
 }
 
 int gdr_linear_fwd(const gdr_linear_args *a, void *stream) {
@@ -1086,7 +1155,7 @@ int gdr_linear_fwd(const gdr_linear_args *a, void *stream) {
     if ((rc = layer_ptr("y", a->y, a->T > 0, e)) || (rc = layer_ptr("ht", a->ht, false, 4))) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a->T == 0) return linear_hand_on(a->h0, a->ht, (size_t)a->n_seqs * a->D, st);
-    const LinSpace sp = linear_space(a->B, a->T, a->D, a->dtype, false);
+    const LinSpace sp = linear_space(a->B, a->T, a->D, false);
     if ((rc = linear_workspace(a, sp, "linear scan forward"))) return rc;
     LinP p;
     LinPlan pl;
@@ -1096,9 +1165,9 @@ int gdr_linear_fwd(const gdr_linear_args *a, void *stream) {
     linear_by_type(a, access, [&](auto t, auto c, auto z, auto k) {
         using E = decltype(t);
         using M = Mem<E, decltype(c)::value>;
-        using H = Shape<E, false>;
-        static_assert(H::kCtas * (6 * H::kRun * M::kRow * H::kWarps + sizeof(Talk<H::kWarps>) + 1024) <= 228 * 1024, "CTAs of an SM");
-        rc = linear_launch(k_linear_fwd<E, decltype(c)::value, decltype(z)::value, decltype(k)::value>, p, pl, H::kCtas, 3 * H::kRun * M::kRow, st);
+        constexpr int kEach = (decltype(z)::value ? 4 : 3) * kFwdRun * M::kRow;
+        static_assert(2 * kWarps * kEach + sizeof(Talk<kWarps * kFwdRun>) <= 227 * 1024, "shared memory");
+        rc = linear_launch(k_linear_fwd<E, decltype(c)::value, decltype(z)::value, decltype(k)::value>, p, pl, 2, kEach, st);
     });
     return rc ? rc : layer_launched("linear scan forward");
 }
@@ -1118,7 +1187,7 @@ int gdr_linear_bwd(const gdr_linear_args *a, void *stream) {
         if ((rc = linear_hand_on(nullptr, a->ddecay, a->D, st))) return rc;
         return linear_hand_on(a->dht, a->dh0, (size_t)a->n_seqs * a->D, st);
     }
-    const LinSpace sp = linear_space(a->B, a->T, a->D, a->dtype, true);
+    const LinSpace sp = linear_space(a->B, a->T, a->D, true);
     if ((rc = linear_workspace(a, sp, "linear scan backward"))) return rc;
     LinP p;
     LinPlan pl;
@@ -1128,10 +1197,9 @@ int gdr_linear_bwd(const gdr_linear_args *a, void *stream) {
     linear_by_type(a, access, [&](auto t, auto c, auto z, auto k) {
         using E = decltype(t);
         using M = Mem<E, decltype(c)::value>;
-        using H = Shape<E, true>;
-        constexpr int kIn = decltype(z)::value ? 5 : 4;
-        static_assert(H::kCtas * (2 * kIn * H::kRun * M::kRow * H::kWarps + sizeof(Talk<H::kWarps>) + sizeof(BackTalk<H::kWarps>) + 1024) <= 228 * 1024, "CTAs of an SM");
-        rc = linear_launch(k_linear_bwd<E, decltype(c)::value, decltype(z)::value, decltype(k)::value>, p, pl, H::kCtas, kIn * H::kRun * M::kRow, st);
+        constexpr int kEach = (decltype(z)::value ? 5 : 4) * kBwdRun * M::kRow;
+        static_assert(3 * kWarps * kEach + sizeof(Talk<kWarps * kBwdRun>) + sizeof(BackTalk) <= 227 * 1024, "shared memory");
+        rc = linear_launch(k_linear_bwd<E, decltype(c)::value, decltype(z)::value, decltype(k)::value>, p, pl, 3, kEach, st);
     });
     if (rc) return rc;
     k_linear_ddecay<<<(unsigned)((a->D + 31) / 32), dim3(32, 32), 0, st>>>(p.part, (long long)p.B * p.chunks, p.D, a->decay, a->ddecay);

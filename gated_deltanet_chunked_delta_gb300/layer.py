@@ -43,7 +43,7 @@ __all__ = ["short_conv", "short_conv_step", "state_space_scan", "state_space_ste
            "gated_residual_rms_norm", "block_matmul_fp8"]
 
 STATE_STRIDE = 16  # GDR_SSM_STRIDE: tokens between the states kept for the backward
-LINEAR_STRIDE = {torch.bfloat16: 48, torch.float32: 24}  # GDR_LINEAR_STRIDE_BF16, _F32
+LINEAR_STRIDE = 48  # GDR_LINEAR_STRIDE
 STATE_SIZES = (8, 16, 32, 64)
 
 _DTYPES = {torch.bfloat16: GDR_BF16, torch.float32: GDR_F32}
@@ -111,8 +111,8 @@ def _calls():
             f = getattr(lib, "gdr_" + name)
             f.argtypes, f.restype = [c_void_p, c_void_p], c_int
         for name, kinds in (("conv_bwd", [c_longlong] * 3 + [c_int]), ("ssm_fwd", [c_void_p]), ("ssm_bwd", [c_void_p]),
-                            ("norm_bwd", [c_longlong] * 2), ("linear_fwd", [c_longlong] * 3 + [c_int]),
-                            ("linear_bwd", [c_longlong] * 3 + [c_int]), ("block_norm_bwd", [c_longlong] * 2)):
+                            ("norm_bwd", [c_longlong] * 2), ("linear_fwd", [c_longlong] * 3),
+                            ("linear_bwd", [c_longlong] * 3), ("block_norm_bwd", [c_longlong] * 2)):
             f = getattr(lib, f"gdr_{name}_workspace_size")
             f.argtypes, f.restype = kinds, c_size_t
         _lib = lib
@@ -499,16 +499,16 @@ def _linear_head(x, input_gate, decay_gate, decay, z, decay_scale, initial_state
 
 
 def _linear_fwd(x, input_gate, decay_gate, decay, z, decay_scale, initial_state, output_final_state, cu_seqlens, keep):
-    dev, code = _linear_check(x, input_gate, decay_gate, decay, z, decay_scale, 2)
+    dev, _ = _linear_check(x, input_gate, decay_gate, decay, z, decay_scale, 2)
     n_seqs = _sequences(x, dev, cu_seqlens)
     (b, t, d), where = x.shape, x.device
     if initial_state is not None:
         _param("initial_state", initial_state, dev, (n_seqs, d))
     y = _empty((b, t, d), dtype=x.dtype, device=where)
     ht = _empty((n_seqs, d), dtype=_F32, device=where) if output_final_state else None
-    states = _empty((b, -(-t // LINEAR_STRIDE[x.dtype]), d), dtype=_F32, device=where) if keep else None
+    states = _empty((b, -(-t // LINEAR_STRIDE), d), dtype=_F32, device=where) if keep else None
     lib = _calls()
-    size = lib.gdr_linear_fwd_workspace_size(b, t, d, code)
+    size = lib.gdr_linear_fwd_workspace_size(b, t, d)
     ws = _empty(size, dtype=torch.uint8, device=where) if size else None
     _run(lib.gdr_linear_fwd,
          _LINEAR.pack(*_linear_head(x, input_gate, decay_gate, decay, z, decay_scale, initial_state, cu_seqlens, n_seqs),
@@ -537,7 +537,7 @@ class _GatedLinearScan(torch.autograd.Function):
         new = lambda like: None if like is None else _empty(like.shape, dtype=like.dtype, device=where)  # noqa: E731
         dx, di, dr, dz, ddecay, dh0 = (new(v) for v in (x, input_gate, decay_gate, z, decay, initial_state))
         lib = _calls()
-        size = lib.gdr_linear_bwd_workspace_size(b, t, d, _DTYPES[x.dtype])
+        size = lib.gdr_linear_bwd_workspace_size(b, t, d)
         ws = _empty(size, dtype=torch.uint8, device=where) if size else None
         _run(lib.gdr_linear_bwd,
              _LINEAR.pack(*_linear_head(x, input_gate, decay_gate, decay, z, ctx.decay_scale, initial_state, cu_seqlens, n_seqs),
@@ -556,8 +556,8 @@ def gated_linear_scan(x, input_gate, decay_gate, decay, z=None, decay_scale=8.0,
     when absent).  Returns (y [B, T, D], final_state [n_seqs, D] fp32 or None); differentiable in every tensor but
     cu_seqlens.
 
-    The workspace, held for the call, is 16 bytes a channel for every 96 tokens (48 in fp32), in the backward 20 bytes for
-    every 48 (24); a forward that keeps a gradient holds states of 4 bytes a channel for every 48 (24) tokens."""
+    The workspace, held for the call, is 16 bytes a channel for every 96 tokens, in the backward 20 bytes for every 48; a
+    forward that keeps a gradient holds states of 4 bytes a channel for every 48 tokens."""
     _no_tangents("gated_linear_scan", x, input_gate, decay_gate, decay, z, initial_state)
     decay_scale = float(decay_scale)
     if _wants_grad(x, input_gate, decay_gate, decay, z, initial_state):

@@ -326,10 +326,9 @@ GDR_API int gdr_ssm_step(const gdr_ssm_step_args *args, void *stream);
  * channel, with s = decay_scale softplus(decay):
  *     a_t = e^{-s sigmoid(decay_gate_t)},
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t,   y_t = h_t silu(z_t) (or h_t).
- * `states` (nullable) keeps h before every 48th (bf16) or 24th (fp32) token of
- * every batch row for the backward. */
-#define GDR_LINEAR_STRIDE_BF16 48
-#define GDR_LINEAR_STRIDE_F32 24
+ * `states` (nullable) keeps h before every 48th token of every batch row for
+ * the backward. */
+#define GDR_LINEAR_STRIDE 48
 typedef struct {
     const void *x, *input_gate, *decay_gate, *z; /* [B, T, D]; z nullable */
     const float *decay;         /* [D] */
@@ -341,7 +340,7 @@ typedef struct {
     int dtype;
     void *y;                    /* [B, T, D] (forward) */
     float *ht;                  /* [n_seqs, D], nullable (forward) */
-    float *states;              /* [B, ceil(T / stride), D]: written by the forward, read by the backward */
+    float *states;              /* [B, ceil(T / 48), D]: written by the forward, read by the backward */
     /* backward */
     const void *dy;             /* [B, T, D] contiguous */
     const float *dht;           /* nullable */
@@ -351,9 +350,9 @@ typedef struct {
     void *workspace;            /* gdr_linear_*_workspace_size bytes, 16-byte aligned (may be null when 0) */
     size_t workspace_bytes;
 } gdr_linear_args;
-GDR_API size_t gdr_linear_fwd_workspace_size(long long B, long long T, long long D, int dtype);
+GDR_API size_t gdr_linear_fwd_workspace_size(long long B, long long T, long long D);
 GDR_API int gdr_linear_fwd(const gdr_linear_args *args, void *stream);
-GDR_API size_t gdr_linear_bwd_workspace_size(long long B, long long T, long long D, int dtype);
+GDR_API size_t gdr_linear_bwd_workspace_size(long long B, long long T, long long D);
 GDR_API int gdr_linear_bwd(const gdr_linear_args *args, void *stream);
 
 /* One token for each of `rows` sequences; slots as in gdr_conv_step. */

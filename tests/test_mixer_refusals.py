@@ -38,7 +38,7 @@ def _linear(**kw):
     (dict(cu_seqlens=P, n_seqs=(1 << 24) + 1), SHAPE), (dict(cu_seqlens=P + 2), ALIGN), (dict(decay_scale=0.0), ARG),
     (dict(decay_scale=-1.0), ARG), (dict(decay_scale=float("inf")), ARG), (dict(decay_scale=float("nan")), ARG), (dict(x=P + 1), ALIGN),
     (dict(z=P + 1), ALIGN), (dict(decay=P + 2), ALIGN), (dict(h0=P + 2), ALIGN), (dict(states=P + 1), ALIGN),
-    (dict(x=P + 2, dtype=1), ALIGN), (dict(workspace=None), WORKSPACE), (dict(workspace=P + 8), ALIGN), (dict(workspace_bytes=16), WORKSPACE)])
+    (dict(x=P + 2, dtype=1), ALIGN)])
 def test_linear_refusals(lib, kw, code):
     assert _call(lib.gdr_linear_fwd, _linear(**kw)) == code
     assert _call(lib.gdr_linear_bwd, _linear(**kw)) == code
@@ -52,21 +52,21 @@ def test_linear_forward_refusals(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dy=None), ARG), (dict(states=None), ARG), (dict(dx=None), ARG), (dict(di=None), ARG), (dict(dr=None), ARG), (dict(dz=None), ARG),
-    (dict(ddecay=None), ARG), (dict(dht=P + 2), ALIGN), (dict(dh0=P + 1), ALIGN)])
+    (dict(ddecay=None), ARG), (dict(dht=P + 2), ALIGN), (dict(dh0=P + 1), ALIGN), (dict(workspace=None), WORKSPACE),
+    (dict(workspace=P + 8), ALIGN), (dict(workspace_bytes=16), WORKSPACE)])
 def test_linear_backward_refusals(lib, kw, code):
     assert _call(lib.gdr_linear_bwd, _linear(**kw)) == code
 
 
 def test_linear_workspace_sizes(lib):
     for f, a in ((lib.gdr_linear_fwd_workspace_size, lib.gdr_linear_fwd), (lib.gdr_linear_bwd_workspace_size, lib.gdr_linear_bwd)):
-        for dtype in (0, 1):
-            need = f(1, 5000, 100, dtype)
-            assert need >= 16 * 100 * -(-5000 // 128) and need % 16 == 0
-            assert _call(a, _linear(T=5000, D=100, workspace_bytes=need - 1, dtype=dtype)) == WORKSPACE
-            assert f(0, 5, 5, dtype) == f(1, -1, 5, dtype) == f(1, 5, 0, dtype) == 0
-            assert f(1, 1 << 20, 1 << 12, dtype) > 1 << 29
-            assert lib.gdr_linear_fwd_workspace_size(1, 1, 100, dtype) == 0  # one chunk needs none
-        assert f(1, 5, 5, 2) == 0
+        need = f(1, 5000, 100)
+        assert need >= 16 * 100 * 5000 // 96 and need % 16 == 0
+        for kw, code in ((dict(workspace=None), WORKSPACE), (dict(workspace=P + 8), ALIGN), (dict(workspace_bytes=need - 1), WORKSPACE)):
+            assert _call(a, _linear(**{**dict(T=5000, D=100), **kw})) == code
+        assert f(0, 5, 5) == f(1, -1, 5) == f(1, 5, 0) == 0
+        assert f(1, 1 << 20, 1 << 12) >= 16 * (1 << 12) * (1 << 20) // 96
+    assert lib.gdr_linear_fwd_workspace_size(1, 1, 100) == 0  # one chunk needs none
 
 
 def _step(cls, **kw):
