@@ -18,6 +18,8 @@
 // pieces of the rows to come to shared memory of its own, asynchronously, so that
 // reads are on their way while a row is reduced, and no thread waits for
 // another's copies.
+#include <string.h>
+
 #include "gdr_layer.h"
 
 namespace {
@@ -33,6 +35,9 @@ struct BlockP {
     long long M, x_row, x_outer, gate_row, gate_outer, res_row, res_outer;
     int D, lanes, inner, depth;  // lanes: threads of a row; depth: rows in shared memory (0: none)
     float scale, eps;
+    // Pairs of constants, read from the parameters: packed instructions take no
+    // immediate operand, and the compiler would make a pair of one at each use.
+    f32x2 neg_log2e, one, minus, scale2;
 };
 
 // Where a row of x, gate and residual begins: `inner` heads of a token have a stride of their own.
@@ -88,33 +93,38 @@ struct Part {
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place + i * blockDim.x * 16) : "memory");
         }
     }
-    static __device__ __forceinline__ void get(const Raw &raw, float (&f)[kN]) {
+    // Elements in pairs, for packed fp32 instructions.
+    static constexpr int kH = kN / 2;
+    static __device__ __forceinline__ void get(const Raw &raw, f32x2 (&f)[kH]) {
 #pragma unroll
-        for (int i = 0; i < kN; i += kV) {
+        for (int i = 0; i < kN; i += kV == 8 ? 8 : 2) {
             if (kV == 8) {
                 float e[8];
                 unpack8(raw.v[i / 8], e);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[i + k < kN ? i + k : 0] = e[k];
+                for (int k = 0; k < 4; ++k) f[i / 2 + k < kH ? i / 2 + k : 0] = mk2(e[2 * k], e[2 * k + 1]);
             } else {
-                f[i] = to_f(raw.s[kV == 8 ? 0 : i]);
+                f[i / 2] = mk2(to_f(raw.s[kV == 8 ? 0 : i]), to_f(raw.s[kV == 8 ? 0 : i + 1]));
             }
         }
     }
-    static __device__ __forceinline__ void store(T *row, int D, int tid, int lanes, const float (&f)[kN]) {
+    static __device__ __forceinline__ void store(T *row, int D, int tid, int lanes, const f32x2 (&f)[kH]) {
+        float e[kN];
+#pragma unroll
+        for (int i = 0; i < kH; ++i) un2(f[i], e[2 * i], e[2 * i + 1]);
         if (kV == 8) {
 #pragma unroll
             for (int i = 0; i < kN / 8; ++i) {
-                float e[8];
+                float v[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) e[k] = f[8 * i + k];
-                store8<T, true>(row + at(8 * i, tid, lanes), e, D - at(8 * i, tid, lanes));
+                for (int k = 0; k < 8; ++k) v[k] = e[8 * i + k];
+                store8<T, true>(row + at(8 * i, tid, lanes), v, D - at(8 * i, tid, lanes));
             }
         } else {
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int c = at(i, tid, lanes);
-                if (c < D) from_f(row[c], f[i]);
+                if (c < D) from_f(row[c], e[i]);
             }
         }
     }
@@ -143,13 +153,19 @@ __device__ __forceinline__ void row_sum(float (&v)[kS], int lanes, float (*buf)[
         for (int s = 0; s < kS; ++s) v[s] += __shfl_xor_sync(0xffffffffu, v[s], m);
 }
 
-// silu(v) and its derivative.
-__device__ __forceinline__ float silu(float v) { return v * sigmoidf(v); }
-__device__ __forceinline__ void silu_both(float v, float &f, float &df) {
-    const float g = sigmoidf(v);
-    f = v * g;
-    df = g * fmaf(v, 1.f - g, 1.f);
+__device__ __forceinline__ f32x2 dup(float v) { return mk2(v, v); }
+__device__ __forceinline__ float both(f32x2 v) {
+    float a, b;
+    un2(v, a, b);
+    return a + b;
 }
+__device__ __forceinline__ f32x2 sigmoid2(const BlockP &p, f32x2 v) {
+    float a, b;
+    un2(mul2(v, p.neg_log2e), a, b);
+    un2(add2(mk2(ex2f(a), ex2f(b)), p.one), a, b);
+    return mk2(rcpf(a), rcpf(b));
+}
+__device__ __forceinline__ f32x2 silu2(const BlockP &p, f32x2 v) { return mul2(v, sigmoid2(p, v)); }
 
 // The rows of a CTA, `group` at a time, from kMost tensors, of which those that
 // are there have a place in each stage.  What a row costs beside its elements
@@ -247,7 +263,7 @@ constexpr int kGate = 1, kStream = 2, kNext = 4;
 
 // Forward: one row a CTA (kCta) or `lanes` lanes of a warp.
 template <typename T, int kV, int kN, int kThreads, bool kCta, int kHas>
-__global__ void __launch_bounds__(kThreads) k_block_fwd(const BlockP p) {
+__global__ void __launch_bounds__(kThreads) k_block_fwd(const __grid_constant__ BlockP p) {
     using P = Part<T, kV, kN>;
     __shared__ float buf[2][1][32];
     const int tid = kCta ? threadIdx.x : threadIdx.x % p.lanes, D = p.D;
@@ -261,41 +277,42 @@ __global__ void __launch_bounds__(kThreads) k_block_fwd(const BlockP p) {
     P::load(static_cast<const T *>(p.x) + from.at(p.x_row, p.x_outer), len, tid, p.lanes, rx);
     if (gate) P::load(static_cast<const T *>(p.gate) + from.at(p.gate_row, p.gate_outer), len, tid, p.lanes, rg);
     if (stream) P::load(static_cast<const T *>(p.residual) + from.at(p.res_row, p.res_outer), len, tid, p.lanes, rr);
-    float v[kN], sum[1] = {0.f};
+    f32x2 v[P::kH], acc = dup(0.f);
     P::get(rx, v);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) sum[0] = fmaf(v[i], v[i], sum[0]);
-    row_sum<1, kCta>(sum, p.lanes, buf[0]);
-    const float inv_x = 1.f / sqrtf(sum[0] / (float)D + p.eps);
-    float g[kN], w[kN];
+    for (int i = 0; i < P::kH; ++i) acc = fma2(v[i], v[i], acc);
+    float sum[1] = {both(acc)};
+    f32x2 g[P::kH], w[P::kH];
     typename Part<float, kV, kN>::Raw rw;
     Part<float, kV, kN>::load(p.weight, D, tid, p.lanes, rw);
     Part<float, kV, kN>::get(rw, w);
+#pragma unroll
+    for (int i = 0; i < P::kH; ++i) v[i] = mul2(v[i], w[i]);
     if (gate) {
         P::get(rg, g);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) w[i] *= silu(g[i]);
+        for (int i = 0; i < P::kH; ++i) v[i] = mul2(v[i], silu2(p, g[i]));
     }
+    row_sum<1, kCta>(sum, p.lanes, buf[0]);
+    const float inv_x = 1.f / sqrtf(sum[0] / (float)D + p.eps);
+    const f32x2 k = dup(p.scale * inv_x);
+    if (stream) P::get(rr, g);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = p.scale * (v[i] * inv_x * w[i]);
-    if (stream) {
-        P::get(rr, g);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] += g[i];
-    }
+    for (int i = 0; i < P::kH; ++i) v[i] = stream ? fma2(v[i], k, g[i]) : mul2(v[i], k);
     P::store(static_cast<T *>(p.r) + row * D, len, tid, p.lanes, v);
     float inv_r = 0.f;
     if (next) {
-        sum[0] = 0.f;
+        // places behind a row's end hold zeros
+        acc = dup(0.f);
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-            if (P::at(i, tid, p.lanes) < D) sum[0] = fmaf(v[i], v[i], sum[0]);
+        for (int i = 0; i < P::kH; ++i) acc = fma2(v[i], v[i], acc);
+        sum[0] = both(acc);
         row_sum<1, kCta>(sum, p.lanes, buf[1]);
         inv_r = 1.f / sqrtf(sum[0] / (float)D + p.eps);
         Part<float, kV, kN>::load(p.next, D, tid, p.lanes, rw);
         Part<float, kV, kN>::get(rw, w);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = v[i] * inv_r * w[i];
+        for (int i = 0; i < P::kH; ++i) v[i] = mul2(mul2(v[i], dup(inv_r)), w[i]);
         P::store(static_cast<T *>(p.y) + row * D, len, tid, p.lanes, v);
     }
     if (p.stats && on && tid == 0) *reinterpret_cast<float2 *>(p.stats + 2 * row) = make_float2(inv_x, inv_r);
@@ -303,15 +320,16 @@ __global__ void __launch_bounds__(kThreads) k_block_fwd(const BlockP p) {
 
 // A CTA keeps its part of the weights' gradients in registers.
 template <typename T, int kV, int kN, int kThreads, bool kCta, int kHas>
-__global__ void __launch_bounds__(kThreads, kThreads == kShort && kN == 8 ? 3 : 1) k_block_bwd(const BlockP p) {
+__global__ void __launch_bounds__(kThreads, kThreads == kShort && kN == 8 ? 3 : 1) k_block_bwd(const __grid_constant__ BlockP p) {
     using P = Part<T, kV, kN>;
     using W = Part<float, kV, kN>;
     extern __shared__ __align__(16) char stages[];
     __shared__ float buf[2][3][32];
     const int tid = kCta ? threadIdx.x : threadIdx.x % p.lanes, D = p.D, group = kCta ? 1 : blockDim.x / p.lanes;
-    float gw[kN], gn[kN];
+    constexpr int kH = P::kH;
+    f32x2 gw[kH], gn[kH];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) gw[i] = gn[i] = 0.f;
+    for (int i = 0; i < kH; ++i) gw[i] = gn[i] = dup(0.f);
     // kHas: the gradients of all outputs are there
     constexpr int kMask = kHas < 0 ? -1 : 1 | (kHas & kGate ? 2 : 0) | ((kHas & kStream) && (kHas & kNext) ? 4 : 0) | 8 | (kHas & kNext ? 16 : 0);
     const bool gate = kHas < 0 ? p.gate != nullptr : kHas & kGate, stream = kHas < 0 ? p.residual != nullptr : kHas & kStream,
@@ -332,10 +350,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == kShort && kN == 8 ? 3 : 
     int turn = 0;
     for (; rows.there(); rows.next(), turn ^= 1) {
         const float2 inv = inv_next;
+        const f32x2 inv_x = dup(inv.x), inv_y = dup(inv.y);
         inv_next = stats(rows.first + rows.step);
         typename P::Raw raw;
         typename W::Raw rw;
-        float n[kN], c[kN], u[kN], r[kN];  // c: n w silu(gate)
+        f32x2 n[kH], c[kH], u[kH], r[kH];  // c: n w silu(gate)
         rows.read(0, raw);
         P::get(raw, n);
         W::load(p.weight, D, tid, p.lanes, rw);
@@ -344,29 +363,29 @@ __global__ void __launch_bounds__(kThreads, kThreads == kShort && kN == 8 ? 3 : 
             rows.read(1, raw);
             P::get(raw, r);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) c[i] *= silu(r[i]);
+            for (int i = 0; i < kH; ++i) c[i] = mul2(c[i], silu2(p, r[i]));
         }
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            n[i] *= inv.x;
-            c[i] *= n[i];
-            u[i] = 0.f;
+        for (int i = 0; i < kH; ++i) {
+            n[i] = mul2(n[i], inv_x);
+            c[i] = mul2(c[i], n[i]);
+            u[i] = dup(0.f);
         }
         if (has_dr) {
             rows.read(3, raw);
             P::get(raw, u);
         }
-        float s[3] = {0.f, 0.f, 0.f};
+        f32x2 s0 = dup(0.f), s1 = s0, s2 = s0;
         if (next) {
 #pragma unroll
-            for (int i = 0; i < kN; ++i) r[i] = 0.f;
+            for (int i = 0; i < kH; ++i) r[i] = dup(0.f);
             if (stream) {
                 rows.read(2, raw);
                 P::get(raw, r);
             }
-            float f[kN], w2[kN];
+            f32x2 f[kH], w2[kH];
 #pragma unroll
-            for (int i = 0; i < kN; ++i) f[i] = 0.f;
+            for (int i = 0; i < kH; ++i) f[i] = dup(0.f);
             if (has_dy) {
                 rows.read(4, raw);
                 P::get(raw, f);
@@ -374,52 +393,59 @@ __global__ void __launch_bounds__(kThreads, kThreads == kShort && kN == 8 ? 3 : 
             W::load(p.next, D, tid, p.lanes, rw);
             W::get(rw, w2);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                r[i] = fmaf(p.scale, c[i], r[i]);
-                gn[i] = fmaf(f[i], r[i] * inv.y, gn[i]);
-                f[i] *= w2[i];
-                s[0] = fmaf(f[i], r[i], s[0]);
-                u[i] = fmaf(inv.y, f[i], u[i]);
-                s[2] = fmaf(r[i], c[i], s[2]);
+            for (int i = 0; i < kH; ++i) {
+                r[i] = fma2(p.scale2, c[i], r[i]);
+                gn[i] = fma2(f[i], mul2(r[i], inv_y), gn[i]);
+                f[i] = mul2(f[i], w2[i]);
+                s0 = fma2(f[i], r[i], s0);
+                u[i] = fma2(inv_y, f[i], u[i]);
+                s2 = fma2(r[i], c[i], s2);
             }
         }
 #pragma unroll
-        for (int i = 0; i < kN; ++i) s[1] = fmaf(u[i], c[i], s[1]);
+        for (int i = 0; i < kH; ++i) s1 = fma2(u[i], c[i], s1);
+        float s[3] = {both(s0), both(s1), both(s2)};
         row_sum<3, kCta>(s, p.lanes, buf[turn]);
         const float k = next ? inv.y * inv.y * inv.y * s[0] / (float)D : 0.f;
         const float mean = p.scale * (s[1] - k * s[2]) / (float)D;  // of b n
+        const f32x2 minus_k = dup(-k);
         if (next) {
 #pragma unroll
-            for (int i = 0; i < kN; ++i) u[i] = fmaf(-k, r[i], u[i]);
+            for (int i = 0; i < kH; ++i) u[i] = fma2(minus_k, r[i], u[i]);
             if (stream) P::store(static_cast<T *>(p.dres) + rows.row * D, rows.len, tid, p.lanes, u);
         }
         W::load(p.weight, D, tid, p.lanes, rw);
-        float w[kN];
+        f32x2 w[kH];
         W::get(rw, w);
+        const f32x2 drop = dup(-mean * inv.x);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) u[i] *= p.scale;
+        for (int i = 0; i < kH; ++i) u[i] = mul2(u[i], p.scale2);
         if (gate) {
-            float g[kN];
+            f32x2 g[kH];
             rows.read(1, raw);
             P::get(raw, g);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                float sl, ds;
-                silu_both(g[i], sl, ds);
-                const float un = u[i] * n[i];
-                gw[i] = fmaf(un, sl, gw[i]);
-                g[i] = un * w[i] * ds;
-                u[i] = inv.x * fmaf(u[i] * w[i], sl, -n[i] * mean);
+            for (int i = 0; i < kH; ++i) {
+                const f32x2 on = sigmoid2(p, g[i]), sl = mul2(g[i], on), ds = fma2(sl, fma2(on, p.minus, p.one), on), un = mul2(u[i], n[i]);
+                gw[i] = fma2(un, sl, gw[i]);
+                g[i] = mul2(mul2(un, w[i]), ds);
+                u[i] = fma2(n[i], drop, mul2(mul2(mul2(u[i], w[i]), sl), inv_x));
             }
             P::store(static_cast<T *>(p.dgate) + rows.row * D, rows.len, tid, p.lanes, g);
         } else {
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                gw[i] = fmaf(u[i], n[i], gw[i]);
-                u[i] = inv.x * (u[i] * w[i] - n[i] * mean);
+            for (int i = 0; i < kH; ++i) {
+                gw[i] = fma2(u[i], n[i], gw[i]);
+                u[i] = fma2(n[i], drop, mul2(mul2(u[i], w[i]), inv_x));
             }
         }
         P::store(static_cast<T *>(p.dx) + rows.row * D, rows.len, tid, p.lanes, u);
+    }
+    float ew[kN], en[kN];
+#pragma unroll
+    for (int i = 0; i < kH; ++i) {
+        un2(gw[i], ew[2 * i], ew[2 * i + 1]);
+        un2(gn[i], en[2 * i], en[2 * i + 1]);
     }
     float *to = p.part + (long long)blockIdx.x * 2 * D;
     if (kCta) {
@@ -427,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == kShort && kN == 8 ? 3 : 
         for (int i = 0; i < kN; ++i) {
             const int c = P::at(i, tid, p.lanes);
             if (c < D) {
-                to[c] = gw[i];
-                to[D + c] = gn[i];
+                to[c] = ew[i];
+                to[D + c] = en[i];
             }
         }
     } else {
@@ -439,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == kShort && kN == 8 ? 3 : 
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
                     const int c = P::at(i, tid, p.lanes);
-                    sums[0][c] = v ? sums[0][c] + gw[i] : gw[i];
-                    sums[1][c] = v ? sums[1][c] + gn[i] : gn[i];
+                    sums[0][c] = v ? sums[0][c] + ew[i] : ew[i];
+                    sums[1][c] = v ? sums[1][c] + en[i] : en[i];
                 }
             __syncthreads();
         }
@@ -478,8 +504,9 @@ BlockPlan block_plan(long long D) {
     if (D <= 128) return {8, 16, kShort, false};
     if (D <= 256) return {8, 32, kShort, false};
     if (D <= 512) return {16, 32, kShort, false};
-    const int n = D <= 8 * kNarrow ? 8 : 16, t = (int)((D + 32 * n - 1) / (32 * n) * 32);
-    return {n, t, t, true};
+    // two CTAs of 256 threads an SM for 4096 channels (the gradient of 8192 x 4096 120 us; one of 512, eight elements a thread, 146)
+    const int t = (int)((D + 511) / 512 * 32);
+    return {16, t, t, true};
 }
 
 // Rows that a thread keeps on their way (none where two have no room), and CTAs: as
@@ -549,28 +576,33 @@ BlockP block_fill(const gdr_block_norm_args *a, const BlockPlan &pl) {
     p.x_outer = a->x_outer; p.gate_outer = a->gate_outer; p.res_outer = a->residual_outer;
     p.D = (int)a->D; p.lanes = pl.lanes; p.inner = (int)a->inner; p.depth = 0;
     p.scale = a->scale; p.eps = a->eps;
+    auto pair = [](float v) {
+        uint32_t bits;
+        memcpy(&bits, &v, sizeof bits);
+        return (f32x2)bits << 32 | bits;
+    };
+    p.neg_log2e = pair(-kLog2e); p.one = pair(1.f); p.minus = pair(-1.f); p.scale2 = pair(a->scale);
     return p;
 }
 
 // f(type, vector, elements, most threads, a CTA a row, what the call has): kernels
-// for what a call has where rows are vectors and of eight elements a thread; with
+// for what a call has where rows are vectors (but for rows of 257 to 512 and of many channels); with
 // the pointers looked at for each row the gradient of 8192 x 4096 takes 169 us, without 133.
 template <typename F>
 void block_by_type(int dtype, bool vec, int has, const BlockPlan &pl, F f) {
     using std::integral_constant;
     auto w = [&](auto t, auto v, auto h) {
         if (!pl.cta && pl.n == 8) f(t, v, integral_constant<int, 8>{}, integral_constant<int, kShort>{}, std::false_type{}, h);
-        else if (pl.cta && pl.n == 8) f(t, v, integral_constant<int, 8>{}, integral_constant<int, kNarrow>{}, std::true_type{}, h);
+        else if (pl.cta && pl.threads <= kNarrow) f(t, v, integral_constant<int, 16>{}, integral_constant<int, kNarrow>{}, std::true_type{}, h);
         else if constexpr (!(decltype(h)::value >= 0)) {
             if (!pl.cta) f(t, v, integral_constant<int, 16>{}, integral_constant<int, kShort>{}, std::false_type{}, h);
-            else if (pl.threads <= kNarrow) f(t, v, integral_constant<int, 16>{}, integral_constant<int, kNarrow>{}, std::true_type{}, h);
             else f(t, v, integral_constant<int, 16>{}, integral_constant<int, kWide>{}, std::true_type{}, h);
         }
     };
     auto k = [&](auto t) {
         const integral_constant<int, 8> eight{};
         if (!vec) w(t, integral_constant<int, 1>{}, integral_constant<int, -1>{});
-        else if (pl.n != 8 || has < 0) w(t, eight, integral_constant<int, -1>{});
+        else if (!(pl.n == 8 || (pl.cta && pl.threads <= kNarrow)) || has < 0) w(t, eight, integral_constant<int, -1>{});
         else if (has == 0) w(t, eight, integral_constant<int, 0>{});
         else if (has == 1) w(t, eight, integral_constant<int, 1>{});
         else if (has == 2) w(t, eight, integral_constant<int, 2>{});
