@@ -213,11 +213,12 @@ GDR_API int gdr_fwd_noalloc(const gdr_shape *shape, gdr_buf q, gdr_buf k, gdr_bu
 /*
  * Layer operators around a recurrent mixer
  * ----------------------------------------
- * What a layer runs before and after its token mixer, and the mixer with a
- * diagonal transition: the short causal convolution, the selective state
- * space scan, the root-mean-square norm of a residual stream (in 8 bits with
- * scales, or in the input's type) and the product of 8-bit activations with
- * 8-bit weights.  Ownership, execution and errors are as above.  Element
+ * What a layer runs before and after its token mixer, mixers with a diagonal
+ * transition, and the delta rule for one token: the short causal convolution,
+ * the selective state space scan, the gated linear recurrence, the
+ * root-mean-square norm of a residual stream (in 8 bits with scales, or in the
+ * input's type), the norm after a block with its gate and the stream, and the
+ * product of 8-bit activations with 8-bit weights.  Ownership, execution and errors are as above.  Element
  * types: `dtype` is GDR_BF16 or GDR_F32 for the activations of a call;
  * parameters, recurrent states and their gradients are fp32 throughout.
  * Activations are [B, T, ...] with a contiguous innermost part and free
