@@ -18,6 +18,12 @@
 // pieces of the rows to come to shared memory of its own, asynchronously, so that
 // reads are on their way while a row is reduced, and no thread waits for
 // another's copies.
+//
+// bf16: 16384 x 4096 with stream and next norm 89 us (6.0 TB/s); 8192 x 4096 with
+// all parts 62 us (5.4 TB/s) and 121 backward (4.5 TB/s); 262144 heads of 128 with
+// their gate 37 us (5.4 TB/s) and 88 (3.8 TB/s).  The backward is bound by
+// instructions, 63 an element of a head (issue slots 63 % used), and by one
+// reduction after another: 16 warps an SM.
 #include <string.h>
 
 #include "gdr_layer.h"
@@ -587,7 +593,7 @@ BlockP block_fill(const gdr_block_norm_args *a, const BlockPlan &pl) {
 
 // f(type, vector, elements, most threads, a CTA a row, what the call has): kernels
 // for what a call has where rows are vectors (but for rows of 257 to 512 and of many channels); with
-// the pointers looked at for each row the gradient of 8192 x 4096 takes 169 us, without 133.
+// the pointers looked at for each row the gradient of 8192 x 4096 took 169 us, without 147.
 template <typename F>
 void block_by_type(int dtype, bool vec, int has, const BlockPlan &pl, F f) {
     using std::integral_constant;

@@ -47,6 +47,24 @@ def test_a_foul_sequence_changes_nothing_of_the_other(gdr, bad, where, value, le
         assert not all(torch.isfinite(t.float()).all() for t in (foul[0], foul[1], *foul[2].values()))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_thousands_of_short_sequences(gdr, dt):  # noqa: F811
+    """More sequences than a warp's lanes, and than their square; many of them empty, some at one place by the hundred."""
+    gen = torch.Generator().manual_seed(98)
+    lengths = torch.randint(0, 4, (1500,), generator=gen).tolist() + [0] * 400 + [70] + [1] * 90 + [0] * 33
+    v, dy, dht = linear_inputs((1, sum(lengths), 5, lengths, True, True), dt, 99)
+    y, ht, g = run_linear(gdr, v, dy, dht, lengths)
+    p = {k: f64(t, True) for k, t in v.items()}
+    h0 = p.pop("initial_state")
+    ry, rht = M.linear(**p, h0=h0, lengths=lengths)
+    p["initial_state"] = h0
+    want = torch.autograd.grad([ry, rht], [p[k] for k in g], [f64(dy), f64(dht)])
+    close(y, ry, linear_tol(70), "y")
+    close(ht, rht, linear_tol(70), "final")
+    for k, w in zip(g, want):
+        close(g[k], w, linear_tol(len(lengths) if k == "decay" else 70), k)
+
+
 def test_nan_stays_in_its_channel_and_row(gdr):  # noqa: F811
     v, dy, dht = linear_inputs((2, 300, 70, None, False, True), "bf16", 82)
     v["decay_gate"][1, 137, 41] = NAN
