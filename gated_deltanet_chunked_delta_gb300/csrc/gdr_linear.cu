@@ -26,13 +26,13 @@
 // A warp works out a tile's action before it finishes the tile before, whose
 // state comes in meanwhile; the tile after is copied to shared memory.
 //
-// bf16: 16384 x 4096 136 us (3.9 TB/s, issue slots 48 % used), 2 x 4096 x 4096 71 us
-// and 138 backward, packed 8192 x 2048 with the output gate 76 and 145; fp32 5003
-// x 1031, packed, gated, read word by word 51 us.  What bounds them: three warps
-// with tokens an SM quarter, whose chains of exponentials, reciprocals and roots
-// leave half the issue slots empty (two tiles a warp take the registers that
-// more warps would need); and, where few channels leave few columns, the way of
-// a state from CTA to CTA (0.5 to 0.9 us a chunk at 17 to 32 columns).
+// bf16: 16384 x 4096 136 us (3.9 TB/s, issue slots 48 % used), 2 x 4096 x 4096 70 us
+// and 137 backward, packed 8192 x 2048 with the output gate 75 and 138 (issue slots
+// 34 %); fp32 5003 x 1031, packed, gated, copied word by word 52 us.  What bounds
+// them: the time of a tile (2 us, packed and gated 4): three warps with tokens an
+// SM quarter, whose chains of exponentials, reciprocals and roots leave half the
+// issue slots empty (two tiles a warp take the registers that more warps would
+// need).
 // Measured against it for 16384 x 4096: a tile finished before the next is begun
 // 174 us; 24 warps with tokens, one tile each at a time, states through the
 // shared memory of clusters 154 us; one reciprocal for both gates, with a branch
@@ -44,7 +44,7 @@ namespace {
 __device__ unsigned g_linear_status;
 
 constexpr int kTile = 64;     // channels of a CTA
-constexpr int kWindow = 8;    // chunks looked back at once
+constexpr int kWindow = 4;    // chunks looked back at once (eight: the packed backward 143 us, four 138)
 constexpr int kPolls = 1 << 20;  // of the records before a chunk, before its wait is given up
 constexpr int kHelpers = 3;   // warps beside those with tokens: one publishes, one looks back, one scouts
 

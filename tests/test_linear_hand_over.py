@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 
 WARPS = 3  # with tokens
-INFOS, WINDOW = 8, 8
+INFOS, WINDOW = 8, 4
 
 
 class Barrier:
