@@ -1103,7 +1103,8 @@ int linear_launch(K *kernel, const LinP &p, const LinPlan &pl, int stages, size_
     const int threads = 32 * (pl.warps + kHelpers);
     const long long grid = std::min<long long>(p.tiles, (long long)layer_sms() * (65536 / (threads * kRegs)));
     const size_t smem = each * pl.warps * (grid < p.tiles ? stages : 1);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the kernel's limit, not this call's need: another thread may set it between this line and the launch
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(each * kWarps * stages));
     if (e != cudaSuccess) return layer_fail(GDR_ERR_CUDA, "linear scan: %s", cudaGetErrorString(e));
     kernel<<<(unsigned)grid, threads, smem, st>>>(p);
     return GDR_OK;
