@@ -521,9 +521,11 @@ struct BlockGrid {
     int depth, ctas;
     size_t smem;
 };
+constexpr size_t block_room(int per_sm) { return (size_t)(224 * 1024) / per_sm - 2048; }  // shared memory of a CTA for rows
+static_assert(block_room(1) + 2 * 32 * 16 * 4 + 2 * 3 * 32 * 4 <= 227 * 1024, "rows, the groups' sums and the rows' sums");
 BlockGrid block_grid(long long M, const BlockPlan &pl, bool vec, int dtype, int streams, int per_sm) {
-    const size_t stage = (size_t)streams * pl.threads * pl.n * (dtype == GDR_BF16 ? 2 : 4), room = (size_t)(224 * 1024) / per_sm - 2048;
-    const int depth = vec ? (int)std::min<size_t>(4, room / stage) : 0;
+    const size_t stage = (size_t)streams * pl.threads * pl.n * (dtype == GDR_BF16 ? 2 : 4);
+    const int depth = vec ? (int)std::min<size_t>(4, block_room(per_sm) / stage) : 0;
     const long long need = (M + pl.rows() - 1) / pl.rows();
     BlockGrid g{};
     g.depth = depth >= 2 ? depth : 0;
@@ -623,7 +625,8 @@ void block_by_type(int dtype, bool vec, int has, const BlockPlan &pl, F f) {
 int block_has(const gdr_block_norm_args *a) { return (a->gate ? kGate : 0) | (a->residual ? kStream : 0) | (a->next_weight ? kNext : 0); }
 template <typename K>
 int block_launch(K *kernel, const BlockP &p, const BlockGrid &g, int threads, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)g.smem);
+    // the most that any call takes, not this call's need: another thread may set it between this line and the launch
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)block_room(1));
     if (e != cudaSuccess) return layer_fail(GDR_ERR_CUDA, "block norm: %s", cudaGetErrorString(e));
     kernel<<<g.ctas, threads, g.smem, st>>>(p);
     return GDR_OK;

@@ -64,3 +64,23 @@ def test_scans_of_two_threads(gdr, backward):  # noqa: F811
     calls = [linear_call(gen, T, 512, backward) for T in (5, 3000)]
     lib = L._calls()
     both(lib.gdr_linear_bwd if backward else lib.gdr_linear_fwd, [c[:2] for c in calls])
+
+
+def test_norm_gradients_of_two_threads(gdr):  # noqa: F811
+    """CTAs of 64 threads and of 256, which run the same kernel."""
+    gen, lib, calls, kept = gen_of(102), L._calls(), [], []
+    for M, D in ((40, 1024), (400, 4096)):
+        x, gate, res, dy, dr = (rand(gen, M, D).bfloat16() for _ in range(5))
+        w, w2 = 1 + 0.1 * rand(gen, D), 1 + 0.1 * rand(gen, D)
+        head = L._block_head(x, w, gate, res, w2, 0.5, 1e-6)
+        y, r = torch.empty_like(x), torch.empty_like(x)
+        stats = torch.empty(M, 2, device="cuda")
+        assert lib.gdr_block_norm_fwd(L._BLOCK_NORM.pack(*head, r.data_ptr(), y.data_ptr(), stats.data_ptr(), *[0] * 9),
+                                      torch.cuda.current_stream().cuda_stream) == 0
+        size = lib.gdr_block_norm_bwd_workspace_size(M, D)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        outs = [torch.empty_like(x) for _ in range(3)] + [torch.empty_like(w) for _ in range(2)]
+        calls.append((L._BLOCK_NORM.pack(*head, 0, 0, stats.data_ptr(), dr.data_ptr(), dy.data_ptr(), *(t.data_ptr() for t in outs),
+                                         ws.data_ptr(), size), outs))
+        kept.append((x, gate, res, dy, dr, w, w2, stats, ws))
+    both(lib.gdr_block_norm_bwd, calls)
