@@ -26,8 +26,8 @@
 // A warp works out a tile's action before it finishes the tile before, whose
 // state comes in meanwhile; the tile after is copied to shared memory.
 //
-// bf16: 16384 x 4096 136 us (3.9 TB/s, issue slots 48 % used), 2 x 4096 x 4096 70 us
-// and 137 backward, packed 8192 x 2048 with the output gate 75 and 138 (issue slots
+// bf16: 16384 x 4096 128 us (4.2 TB/s, issue slots 48 % used), 2 x 4096 x 4096 67 us
+// and 132 backward, packed 8192 x 2048 with the output gate 75 and 139 (issue slots
 // 34 %); fp32 5003 x 1031, packed, gated, copied word by word 52 us.  What bounds
 // them: the time of a tile (2 us, packed and gated 4): three warps with tokens an
 // SM quarter, whose chains of exponentials, reciprocals and roots leave half the
@@ -67,7 +67,7 @@ struct LinP {
     float scale;
     // Pairs of constants, read from the parameters: packed instructions take no
     // immediate operand, and the compiler would make a pair of one at each use.
-    f32x2 neg_log2e, one, minus, low, poly[5];
+    f32x2 neg_log2e, one, minus, poly[4];
 };
 
 __host__ __device__ __forceinline__ f32x2 pair_of(float v) {
@@ -103,28 +103,33 @@ __device__ __forceinline__ f32x2 rsqrt_2(f32x2 v) {
 __device__ __forceinline__ f32x2 sigmoid2(const LinP &p, f32x2 v) {
     return each(add2(ex2_2(mul2(v, p.neg_log2e)), p.one), [](float x) { return rcpf(x); });
 }
-// a = e^{-s sig}.  The argument of ex2.approx is moved up by 1.5e-8 of the result,
-// which it lies low by on average (a slow state multiplies hundreds of decays);
-// ex2.approx(2.2e-8) is 1 (measured), so that a closed gate changes nothing.
-__device__ __forceinline__ f32x2 decay2(const LinP &p, f32x2 sig, f32x2 neg_s2) { return ex2_2(fma2(sig, neg_s2, p.low)); }
-// 1 - a^2 = 1 - e^-v, v = 2 s sig.  The difference loses its
-// leading digits for small v: below 1/2 by a polynomial of (1 - e^-v) / v
-// (interpolated at the Chebyshev points of [0, 1/2], off by at most 1.5e-9 of
-// it).  kSmall: no v of the call's channel tile reaches 1/2.
+// a = e^-u and 1 - a^2, u = s sig.  Below u = 1/4, where a state multiplies many
+// decays and 1 - a^2 would lose its leading digits, both come from w = 1 - e^-u = u q(u),
+// q a polynomial of degree 4 (least error, off by at most 3.1e-9 of it): a = 1 - w
+// rounds once, to nearest, and 1 - a^2 = w (1 + a).  ex2.approx would leave every
+// decay off by 0.5e-8 to 3e-8 on average (measured, by ranges of its argument),
+// and more by chance: 4096 tokens' states by 1.2e-6 (norm-wise) instead of 2e-7.
+// Above 1/4 a state soon forgets that.  kSmall: no u of the call's channel tile
+// reaches 1/4.
 template <bool kSmall>
-__device__ __forceinline__ f32x2 rest2(const LinP &p, f32x2 v, f32x2 a) {
-    f32x2 q = fma2(v, p.poly[4], p.poly[3]);
-    q = fma2(v, q, p.poly[2]);
-    q = fma2(v, q, p.poly[1]);
-    q = fma2(v, q, p.poly[0]);
-    q = fma2(v, q, p.one);
-    q = mul2(v, q);
-    if (kSmall) return q;
-    float v0, v1, a0, a1, q0, q1;
-    un2(v, v0, v1);
+__device__ __forceinline__ void decay2(const LinP &p, f32x2 u, f32x2 &a, f32x2 &rest) {
+    f32x2 q = fma2(u, p.poly[3], p.poly[2]);
+    q = fma2(u, q, p.poly[1]);
+    q = fma2(u, q, p.poly[0]);
+    q = fma2(u, q, p.one);
+    const f32x2 w = mul2(u, q);
+    a = fma2(w, p.minus, p.one);
+    rest = fma2(w, a, w);
+    if (kSmall) return;
+    float u0, u1, a0, a1, b0, b1, r0, r1;
+    un2(u, u0, u1);
     un2(a, a0, a1);
-    un2(q, q0, q1);
-    return mk2(v0 < 0.5f ? q0 : fmaf(-a0, a0, 1.f), v1 < 0.5f ? q1 : fmaf(-a1, a1, 1.f));
+    un2(ex2_2(mul2(u, p.neg_log2e)), b0, b1);
+    un2(rest, r0, r1);
+    a0 = u0 < 0.25f ? a0 : b0;
+    a1 = u1 < 0.25f ? a1 : b1;
+    a = mk2(a0, a1);
+    rest = mk2(u0 < 0.25f ? r0 : fmaf(-a0, a0, 1.f), u1 < 0.25f ? r1 : fmaf(-a1, a1, 1.f));
 }
 
 // How tokens act on the state before them: h -> a h + b, or h -> b (a < 0)
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_fwd(const __grid_constan
         const Info<kTok> &at = s.info[k % kInfos];
         if (at.tile >= p.tiles) return;
         const int turn = k & 1, d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), t0 = (at.chunk * warps + warp) * kRun;
-        const f32x2 sv = mk2(at.s[lane].x, at.s[lane].y), neg_s2 = mul2(sv, p.neg_log2e), two_s = add2(sv, sv);
+        const f32x2 sv = mk2(at.s[lane].x, at.s[lane].y);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         const char *in = own + turn * other;
@@ -598,9 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_fwd(const __grid_constan
                 const f32x2 i = M::get(in + kStep + j * M::kRow, kAcc == 2 ? ti + at.b * p.i_batch + tt * p.i_row + at.d0 : nullptr);
                 const f32x2 x = M::get(in + 2 * kStep + j * M::kRow, kAcc == 2 ? tx + at.b * p.x_batch + tt * p.x_row + at.d0 : nullptr);
                 const f32x2 sr = sigmoid2(p, r), si = sigmoid2(p, i);
-                o.a[j] = decay2(p, sr, neg_s2);
-                const f32x2 m = sqrt_2(rest2<decltype(sm)::value>(p, mul2(sr, two_s), o.a[j]));
-                o.b[j] = mul2(m, mul2(si, x));
+                f32x2 rest;
+                decay2<decltype(sm)::value>(p, mul2(sr, sv), o.a[j], rest);
+                o.b[j] = mul2(sqrt_2(rest), mul2(si, x));
                 const int q = C ? at.first[C ? warp * kRun + j : 0] : -1;
                 if (C && q >= 0) {
                     if (p.h0) o.b[j] = fma2(o.a[j], load_f(p.h0 + (long long)q * p.D + d, nch), o.b[j]);
@@ -778,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_bwd(const __grid_constan
         const Info<kTok> &at = s.info[k % kInfos];
         if (at.tile >= p.tiles) return;
         const int turn = k & 1, d = at.d0 + 2 * lane, nch = max(0, min(2, p.D - d)), t0 = (at.chunk * warps + warp) * kRun, n = min(kRun, p.T - t0);
-        const f32x2 neg_s = mul2(mk2(at.s[lane].x, at.s[lane].y), p.minus), neg_s2 = mul2(mk2(at.s[lane].x, at.s[lane].y), p.neg_log2e);
+        const f32x2 sv = mk2(at.s[lane].x, at.s[lane].y);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
         char *in = own + k % 3 * other;
@@ -801,14 +806,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_bwd(const __grid_constan
             for (int j = 0; j < kRun; ++j) {
                 const f32x2 sr = sigmoid2(p, get(at, in, 0, j)), si = sigmoid2(p, get(at, in, 1, j));
                 M::put2(in + kStep + j * M::kRow, in + j * M::kRow, si);  // it waits in the place of both gates
-                const f32x2 a = decay2(p, sr, neg_s2), L = mul2(sr, neg_s), v = mul2(add2(L, L), p.minus);
-                // a gate is not quite closed here (1e-36), so that m has a reciprocal
-                const f32x2 rest = add2(rest2<decltype(sm)::value>(p, v, a), dup(1e-36f)), inv = rsqrt_2(rest);
+                const f32x2 u = mul2(sr, sv);
+                f32x2 a, rest;
+                decay2<decltype(sm)::value>(p, u, a, rest);
+                rest = add2(rest, dup(1e-36f));  // a gate is not quite closed here, so that m has a reciprocal
+                const f32x2 inv = rsqrt_2(rest);
                 const f32x2 mi = mul2(mul2(rest, inv), si), b = mul2(mi, get(at, in, 2, j));
                 o.a[j] = a;
                 o.mi[j] = mi;
                 o.sr[j] = sr;
-                o.g[j] = mul2(mul2(mul2(a, a), mul2(L, inv)), mul2(si, p.minus));
+                o.g[j] = mul2(mul2(mul2(a, a), mul2(u, inv)), si);
                 const int q = C ? at.first[C ? warp * kRun + j : 0] : -1;
                 if (C && q >= 0) {
                     B = fma2(a, given(p.h0, q), b);
@@ -972,9 +979,9 @@ __global__ void __launch_bounds__(kStepThreads) k_linear_step(const __grid_const
         float *st = p.state + slot * p.D + d;
         const f32x2 before = load_f(st, nch);
         const f32x2 s = each(load_f(p.decay + d, nch), [&](float v) { return p.scale * softplusf(v); });
-        const f32x2 sr = sigmoid2(p.c, r), a = decay2(p.c, sr, mul2(s, p.c.neg_log2e));
-        const f32x2 m = sqrt_2(rest2<false>(p.c, mul2(add2(s, s), sr), a));
-        y = fma2(a, before, mul2(m, mul2(sigmoid2(p.c, i), x)));
+        f32x2 a, rest;
+        decay2<false>(p.c, mul2(sigmoid2(p.c, r), s), a, rest);
+        y = fma2(a, before, mul2(sqrt_2(rest), mul2(sigmoid2(p.c, i), x)));
         store_f(st, y, nch);
         if (p.z) y = mul2(y, mul2(z, sigmoid2(p.c, z)));
     }
@@ -995,9 +1002,8 @@ LinP linear_constants() {
     p.neg_log2e = pair_of(-kLog2e);
     p.one = pair_of(1.f);
     p.minus = pair_of(-1.f);
-    p.low = pair_of(2.2e-8f);
-    const float poly[5] = {-4.9999982e-1f, 1.6666242e-1f, -4.1630073e-2f, 8.1896136e-3f, -1.1234042e-3f};
-    for (int i = 0; i < 5; ++i) p.poly[i] = pair_of(poly[i]);
+    const float poly[4] = {-4.99999642e-1f, 1.66652888e-1f, -4.15001325e-2f, 7.53017422e-3f};
+    for (int i = 0; i < 4; ++i) p.poly[i] = pair_of(poly[i]);
     return p;
 }
 
