@@ -20,10 +20,15 @@
 // another's copies.
 //
 // bf16: 16384 x 4096 with stream and next norm 89 us (6.0 TB/s); 8192 x 4096 with
-// all parts 62 us (5.4 TB/s) and 121 backward (4.5 TB/s); 262144 heads of 128 with
-// their gate 37 us (5.4 TB/s) and 88 (3.8 TB/s).  The backward is bound by
-// instructions, 63 an element of a head (issue slots 63 % used), and by one
-// reduction after another: 16 warps an SM.
+// all parts 62 us (5.4 TB/s) and 121 backward (4.4 TB/s); 262144 heads of 128 with
+// their gate 37 us (5.5 TB/s) and 88 (3.8 TB/s).  The backward is bound by
+// instructions, 63 an element of a head (issue slots 62 % used, 24 warps an SM; at
+// 4096 channels 47 %, 16 warps), and by one reduction after another.
+// Plans that these figures do not speak for, 33.5 million elements with all parts,
+// backward, bf16 | fp32: 512 channels 147 | 252 us and 1024 channels 178 | 333 (one
+// or four small CTAs an SM), above 8192 channels 391 | 596 (threads at 64
+// registers, which spill), rows that are not whole vectors on 16-byte
+// boundaries 683 to 752 | 617 to 677 (element by element, no rows ahead, spills).
 #include <string.h>
 
 #include "gdr_layer.h"
@@ -533,7 +538,9 @@ BlockGrid block_grid(long long M, const BlockPlan &pl, bool vec, int dtype, int 
     g.ctas = (int)std::max(1LL, std::min(need, (long long)per_sm * layer_sms()));
     return g;
 }
-// CTAs of an SM of the backward: as registers allow.
+// CTAs of an SM of the backward: as many as registers allow of the threads that a
+// kernel may have at most (512; 64-thread CTAs of 513 to 1024 channels would fit
+// eight times, and take four).
 int block_per_sm(const BlockPlan &pl) {
     if (!pl.cta) return pl.n == 8 ? 3 : 1;
     return std::max(1, std::min(4, 512 / pl.threads));
@@ -594,8 +601,10 @@ BlockP block_fill(const gdr_block_norm_args *a, const BlockPlan &pl) {
 }
 
 // f(type, vector, elements, most threads, a CTA a row, what the call has): kernels
-// for what a call has where rows are vectors (but for rows of 257 to 512 and of many channels); with
-// the pointers looked at for each row the gradient of 8192 x 4096 took 169 us, without 147.
+// for what a call has where rows are vectors; with the pointers looked at for each
+// row the gradient of 8192 x 4096 took 169 us, without 147.  Rows of 257 to 512
+// channels and of more than 8192 have only the kernel that looks: each plan's own
+// set is sixteen more kernels to build, whose gain there was not measured.
 template <typename F>
 void block_by_type(int dtype, bool vec, int has, const BlockPlan &pl, F f) {
     using std::integral_constant;

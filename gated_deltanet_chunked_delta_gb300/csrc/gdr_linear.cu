@@ -27,12 +27,16 @@
 // state comes in meanwhile; the tile after is copied to shared memory.
 //
 // bf16: 16384 x 4096 128 us (4.2 TB/s, issue slots 48 % used), 2 x 4096 x 4096 67 us
-// and 132 backward, packed 8192 x 2048 with the output gate 75 and 139 (issue slots
-// 34 %); fp32 5003 x 1031, packed, gated, copied word by word 52 us.  What bounds
+// and 132 backward (54 %), packed 8192 x 2048 with the output gate 74 and 139 (issue
+// slots 32 and 35 %); fp32 2 x 4096 x 2048 56 us and 86 (5.5 TB/s).  What bounds
 // them: the time of a tile (2 us, packed and gated 4): three warps with tokens an
 // SM quarter, whose chains of exponentials, reciprocals and roots leave half the
 // issue slots empty (two tiles a warp take the registers that more warps would
-// need).
+// need).  Next is the special-function pipe: two ex2 (4 cycles a warp), two
+// reciprocals and a root (8 each) an element are 58 us of 16384 x 4096.
+// Rows off 16-byte boundaries are copied word by word: 6144 x 1026 bf16 31 us and 42
+// (1024: 24 and 36), fp32 of 1031 channels 44 and 57 (1024: 31 and 41); bf16 rows off
+// word boundaries also read and write two bytes at a time: 6144 x 1031 82 and 102.
 // Measured against it for 16384 x 4096: a tile finished before the next is begun
 // 174 us; 24 warps with tokens, one tile each at a time, states through the
 // shared memory of clusters 154 us; one reciprocal for both gates, with a branch

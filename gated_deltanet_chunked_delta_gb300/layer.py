@@ -311,8 +311,8 @@ def short_conv(x, weight, bias=None, activation="silu", initial_state=None, outp
 
 def short_conv_step(x, weight, state, bias=None, activation="silu", slots=None):
     """One token of every row: x [rows, D]; state [n_slots, W - 1, D] in x's dtype, updated in place; slots [rows]
-    int32 names each row's state (row r uses slot r when absent), a negative one an idle row whose y is zero.
-    Returns y [rows, D].  No gradient."""
+    int32 names each row's state (row r uses slot r when absent), a negative one an idle row whose y is zero; a state is
+    named at most once.  Returns y [rows, D].  No gradient."""
     silu = _activation(activation)
     _no_tangents("short_conv_step", x, weight, state, bias)
     dev, code = _inputs("x", x)
@@ -555,6 +555,9 @@ def gated_linear_scan(x, input_gate, decay_gate, decay, z=None, decay_scale=8.0,
     (y_t = h_t without z).  x, input_gate, decay_gate, z [B, T, D]; decay [D] fp32; initial_state [n_seqs, D] fp32 (zeros
     when absent).  Returns (y [B, T, D], final_state [n_seqs, D] fp32 or None); differentiable in every tensor but
     cu_seqlens.
+
+    Every token's input is scaled by sqrt(1 - a_t^2), a sequence's first one too: a model that leaves that one unscaled
+    divides its x by sqrt(1 - a_1^2) beforehand.  The output gate is silu; for another one leave z out and multiply y.
 
     The workspace, held for the call, is 16 bytes a channel for every 96 tokens, in the backward 20 bytes for every 48; a
     forward that keeps a gradient holds states of 4 bytes a channel for every 48 tokens."""
